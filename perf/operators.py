@@ -262,7 +262,7 @@ def _run_pages(st):
         if st["compact"]:
             moved = mr.pages_compact(*pool, st["pools"])
             return {"refcount": pool[0], "tables": pool[1], "lens": pool[2], "moved": moved, "pools": st["pools"]}
-        mr.pages_free(*pool, st["done"], st["bs"])
+        mr.pages_free(*pool, st["done"])
         grown = mr.pages_grow(*pool, st["new"], st["new_lens"], st["bs"])
         forked = mr.pages_fork(*pool, st["src"], st["dst"], st["bs"], st["pools"])
         return {"refcount": pool[0], "tables": pool[1], "lens": pool[2], "grown": grown, "forked": forked,
