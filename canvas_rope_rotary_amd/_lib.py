@@ -22,7 +22,9 @@ EXPORTS = ("mrope_abi_version", "mrope_status_string", "mrope_last_error", "mrop
            "mrope_workspace_bytes",
            "mrope_workspace_init", "mrope_planes", "mrope_apply", "mrope_apply_ids", "mrope_apply_ids_noalloc",
            "mrope_apply_kv",
-           "mrope_apply_ids_kv", "mrope_decode")
+           "mrope_apply_ids_kv", "mrope_decode", "mrope_apply_kv8", "mrope_decode_kv8",
+           "mrope_attend_kv8_workspace_bytes", "mrope_attend_kv8", "mrope_pages_workspace_bytes", "mrope_pages_grow",
+           "mrope_pages_free", "mrope_pages_fork", "mrope_pages_compact", "mrope_pages_copy")
 
 
 HOOK_FUSED_CHUNKED = 1
@@ -46,6 +48,12 @@ class MropeError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(message)
         self.status = status
+
+
+class MropePool(ctypes.Structure):
+    """One paged tensor of the page calls (mrope_pool)."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -95,6 +103,28 @@ def load():
     lib.mrope_decode.argtypes = [P, I64, I64, I32, P, I64, I64, I32, P, I64, I64, I32, P, P, *cache,
                                  I32, I32, I32, F64, P]
     lib.mrope_decode.restype = ctypes.c_int
+    tables = [P, I64, I32]  # block_tables, table_stride, table_width
+    kv8 = [P, P, P, P, I32, I64, I64, I64, I64]  # caches, scales, block_size, num_blocks, strides
+    heads = [P, I64, I64, I32]  # pointer, token stride, head stride, heads
+    lib.mrope_apply_kv8.argtypes = [*heads, *heads, P, I64, I64, I64, I32, I32, I32, P, I64, F64, P, I32, P, *tables, *kv8, P]
+    lib.mrope_apply_kv8.restype = ctypes.c_int
+    lib.mrope_decode_kv8.argtypes = [*heads, *heads, P, I64, I64, I32, P, P, *tables, *kv8, I32, I32, I32, F64, P]
+    lib.mrope_decode_kv8.restype = ctypes.c_int
+    lib.mrope_attend_kv8_workspace_bytes.argtypes = [I64, I32, I32, I32, I32, I32, I32, I32, I32]
+    lib.mrope_attend_kv8_workspace_bytes.restype = U64
+    lib.mrope_attend_kv8.argtypes = [*heads, I64, I32, I32, I32, P, I32, P, *tables, *kv8, F64, P, I64, I64, P, P, U64, P]
+    lib.mrope_attend_kv8.restype = ctypes.c_int
+    lib.mrope_pages_workspace_bytes.argtypes = [I64, I64]
+    lib.mrope_pages_workspace_bytes.restype = U64
+    state = [P, I64, *tables, P, I64]  # refcount, num_blocks, tables, seq_lens, n_rows
+    pools = [ctypes.POINTER(MropePool), I32]
+    lib.mrope_pages_grow.argtypes = [*state, I32, P, P, I32, P, P, U64, P]
+    lib.mrope_pages_free.argtypes = [*state, P, I32, P]
+    lib.mrope_pages_fork.argtypes = [*state, I32, P, P, I32, P, *pools, P, U64, P]
+    lib.mrope_pages_compact.argtypes = [*state, P, *pools, P, U64, P]
+    lib.mrope_pages_copy.argtypes = [*pools, I64, P, P, I32, P]
+    for f in (lib.mrope_pages_grow, lib.mrope_pages_free, lib.mrope_pages_fork, lib.mrope_pages_compact, lib.mrope_pages_copy):
+        f.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -107,6 +137,8 @@ def _check(status: int):
 
 # While prepare() runs a binding function, the C calls it would make are recorded here instead.
 _recording: list | None = None
+# Tensors that the recorded calls need alive (workspaces): kept by the PreparedCall.
+_held: list = []
 
 
 class _EpochSlot:
@@ -547,10 +579,11 @@ class PreparedCall:
     with a workspace takes a fresh epoch each time.  `result` is what the binding function returned
     (the same output tensors are written by every run)."""
 
-    __slots__ = ("_dev", "_calls", "result")
+    __slots__ = ("_dev", "_calls", "_held", "result")
 
-    def __init__(self, dev, calls, result):
+    def __init__(self, dev, calls, result, held=()):
         self._dev = dev
+        self._held = held
         self._calls = []
         for cfunc, args in calls:
             # arguments as ctypes values of the declared types: ctypes then converts nothing per call
@@ -559,7 +592,7 @@ class PreparedCall:
                 if isinstance(a, _EpochSlot):
                     slots.append((t(0), a.ws))
                     conv.append(slots[-1][0])
-                elif a is None or isinstance(a, ctypes._SimpleCData):
+                elif a is None or isinstance(a, (ctypes._SimpleCData, ctypes.Array)):
                     conv.append(a)
                 else:
                     conv.append(t(a))
@@ -577,22 +610,22 @@ class PreparedCall:
 
 
 def prepare(fn, *args, **kwargs) -> PreparedCall:
-    """Check and marshal a call of one of this module's functions (planes, apply, apply_ids,
-    apply_ids_noalloc, apply_kv, apply_ids_kv, decode) once, without launching it, and return a
+    """Check and marshal a call of one of this package's functions (planes, apply, apply_ids,
+    apply_ids_noalloc, apply_kv, apply_ids_kv, decode, and those of the 8-bit cache and its pages) once, without launching it, and return a
     PreparedCall that launches it each time it is called -- for an eager loop that repeats a call on
     the same buffers (a decode step), where the per-call argument checks would otherwise cost more
     host time than the GPU work.  The stream current now is the one every run launches on.  Output
     tensors the call would allocate are allocated here once.  The prepared call must not be run
     inside HIP-graph capture (capture the plain call instead: its epochs come from the device)."""
-    global _recording
+    global _recording, _held
     if _recording is not None:
         raise RuntimeError("prepare() does not nest")
     rec = []
-    _recording = rec
+    _recording, _held = rec, []
     try:
         result = fn(*args, **kwargs)
     finally:
-        _recording = None
+        held, _recording, _held = _held, None, []
     if not rec:
         raise ValueError(f"{getattr(fn, '__name__', fn)} made no library call to prepare")
     dev = None
@@ -600,4 +633,4 @@ def prepare(fn, *args, **kwargs) -> PreparedCall:
         if isinstance(a, torch.Tensor) and a.is_cuda:
             dev = a.device
             break
-    return PreparedCall(dev, rec, result)
+    return PreparedCall(dev, rec, result, held)

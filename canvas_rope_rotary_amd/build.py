@@ -3,12 +3,15 @@ from __future__ import annotations
 
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmrope.so")
-SOURCES = ["mrope_kernels.hip", "mrope_abi.hip"]
+OBJ = os.path.join(PKG, "_build")
+SOURCES = ["mrope_kernels.hip", "mrope_abi.hip", "mrope_append.hip", "mrope_attend.hip", "mrope_pages.hip",
+           "mrope_kv8_abi.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -24,20 +27,30 @@ HIPCC_FLAGS = [
 
 
 def build(verbose: bool = False) -> str:
+    """Compile every source (one hipcc each, in parallel) and link the library."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    os.makedirs(OBJ, exist_ok=True)
+    objs = [os.path.join(OBJ, s + ".o") for s in SOURCES]
+    inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
+    with ThreadPoolExecutor(4) as ex:
+        msgs = list(ex.map(lambda so: _run([hipcc, *(f for f in HIPCC_FLAGS if f != "-shared"), *inc, "-c", os.path.join(CSRC, so[0]), "-o", so[1]]),
+                           zip(SOURCES, objs)))
     tmp = LIB + ".tmp"
-    cmd = [hipcc, *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp,
-           *[os.path.join(CSRC, s) for s in SOURCES]]
+    msgs.append(_run([hipcc, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]))
+    if verbose and any(msgs):
+        print("\n".join(m for m in msgs if m))
+    os.replace(tmp, LIB)
+    return LIB
+
+
+def _run(cmd) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     # hipcc's host pass does not know the packed-fp32 feature and says so; that line is harmless.
     noise = "is not a recognized feature for this target"
     msgs = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if noise not in l and l.strip())
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{msgs}")
-    if verbose and msgs:
-        print(msgs)
-    os.replace(tmp, LIB)
-    return LIB
+    return msgs
 
 
 if __name__ == "__main__":

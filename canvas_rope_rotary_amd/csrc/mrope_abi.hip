@@ -19,9 +19,9 @@ int test_hooks() { return g_test_hooks.load(std::memory_order_relaxed); }
 }  // namespace mrope
 
 
-namespace {
+namespace mrope {
 
-thread_local char g_last_error[512] = "";
+static thread_local char g_last_error[512] = "";
 
 mrope_status fail(mrope_status st, const char *fmt, ...)
 {
@@ -38,7 +38,7 @@ mrope_status hip_status(hipError_t e, const char *what)
     return fail(MROPE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Rotary constants for rot_dim = 64.
 //   inv_freq[j] = 1 / theta^(2j/64): the power in double rounded once to fp32, the reciprocal one
@@ -91,6 +91,10 @@ mrope_status check_heads(void *q, int64_t q_tok, int64_t q_head, int32_t nq, voi
     if (nk > 0 && k_head < head_dim && nk > 1) return fail(MROPE_ERR_ARG, "k_head_stride < head_dim");
     return MROPE_OK;
 }
+
+}  // namespace mrope
+
+namespace {
 
 Heads make_heads(void *q, int64_t q_tok, int64_t q_head, int32_t nq, void *k, int64_t k_tok, int64_t k_head, int32_t nk,
                  int64_t n_tokens, int32_t head_dim, void *q_out, void *k_out)

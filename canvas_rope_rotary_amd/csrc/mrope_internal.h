@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mrope.h"
+
 namespace mrope {
 
 constexpr int kMaxHeads = 64;
@@ -112,6 +114,15 @@ struct DecodeArgs {
     const int32_t *amount;
     PagedKV kv;
 };
+
+// Host helpers of the C ABI files: the status of a refused call (with its text), of a HIP result, the
+// rotary constants, and the checks of Q/K heads.
+mrope_status fail(mrope_status st, const char *fmt, ...);
+mrope_status hip_status(hipError_t e, const char *what);
+Rotary make_rotary(double theta);
+mrope_status check_heads(void *q, int64_t q_tok, int64_t q_head, int32_t nq, void *k, int64_t k_tok, int64_t k_head,
+                         int32_t nk, int64_t n_tokens, int32_t head_dim, int32_t rot_dim, int32_t dtype, void *q_out,
+                         void *k_out);
 
 hipError_t launch_workspace_init(void *ws, size_t bytes, hipStream_t stream);
 hipError_t launch_text_scalars(const Scan &s, hipStream_t stream);

@@ -320,6 +320,171 @@ mrope_status mrope_decode(void *q, int64_t q_tok_stride, int64_t q_head_stride, 
                           int64_t cache_block_stride, int64_t cache_tok_stride, int64_t cache_head_stride,
                           int32_t head_dim, int32_t rot_dim, int32_t dtype, double theta, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Paged K/V cache in 8 bits (mrope_apply_kv8, mrope_decode_kv8, mrope_attend_kv8).
+ *
+ * k_cache, v_cache  e4m3 codes (OCP 8-bit float: 1 sign, 4 exponent, 3 mantissa bits, largest 448, no
+ *            infinities), element (block, row, head, d) at block*cache_block_stride +
+ *            row*cache_tok_stride + head*cache_head_stride + d bytes; both caches use these strides.
+ * k_scale, v_scale  [num_blocks][n_kv_heads] fp32, one scale for each block (page) and head: a code
+ *            stands for code * scale.  Scales are powers of two in [2^-96, 2^120].
+ * block_tables  int32, row s at s*table_stride: entry i is the page that holds positions
+ *            [i*block_size, (i + 1)*block_size) of sequence s; table_width entries may be read.  A
+ *            page outside [0, num_blocks), and a position past the table, holds nothing: it is not
+ *            written and not attended to.
+ * block_size 16, 32 or 64.  head_dim 64, 128 or 256.  n_kv_heads 1..64.
+ * Alignment: caches 16-byte aligned, cache strides multiples of 16 bytes.  The caches and scales must
+ *            not overlap q, k, v or out.
+ *
+ * What an append writes.  A call that writes positions [a, b) of a sequence into a page, in which the
+ * sequence already holds the h positions before a, gives the page (for K and for V, for each head)
+ *   e = the smallest exponent with (largest finite |x| of the new rows) <= 448 * 2^e, at least -96,
+ *       and if h > 0 at least the exponent of the scale found there;
+ *   scale = 2^e; new rows: code = x * 2^-e rounded once to e4m3 (nearest even), x being the fp32
+ *       value (K: rotated, rounded once to fp32 as in mrope_apply); the h rows already there, if their
+ *       scale was smaller: code * (old scale / new scale), rounded to e4m3 (exact but for codes that
+ *       fall below e4m3's normal range).
+ * Rows of the page that hold no position yet stay as they are.  A value that is not finite is stored
+ * as NaN and has no part in the scale.  A page that two sequences share must not be appended to (fork
+ * its last page first, see mrope_pages_fork): two writers of one page race.
+ * ------------------------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------------------------
+ * mrope_apply_kv8 -- mrope_apply_kv for the 8-bit cache: Q rotated in place, K rotated and V written
+ * as e4m3 codes.  Arguments as in mrope_apply_kv, but the destination is given by sequence:
+ * cu_seqlens [n_seqs + 1] as in mrope_planes (tokens behind cu_seqlens[n_seqs] are left as they are),
+ * pos_offset [n_seqs] int32 (nullable = all 0) the position of each sequence's first token of this
+ * call, and the block tables above: token i of sequence s goes to position pos_offset[s] + i.  A
+ * sequence with a negative pos_offset has its Q rotated and nothing written.  v is required.
+ * One launch, one workgroup a page.
+ * ------------------------------------------------------------------------------------------- */
+mrope_status mrope_apply_kv8(void *q, int64_t q_tok_stride, int64_t q_head_stride, int32_t n_q_heads, const void *k,
+                             int64_t k_tok_stride, int64_t k_head_stride, int32_t n_kv_heads, const void *v,
+                             int64_t v_tok_stride, int64_t v_head_stride, int64_t n_tokens, int32_t head_dim,
+                             int32_t rot_dim, int32_t dtype, const int32_t *planes, int64_t plane_stride, double theta,
+                             const int32_t *cu_seqlens, int32_t n_seqs, const int32_t *pos_offset,
+                             const int32_t *block_tables, int64_t table_stride, int32_t table_width, void *k_cache,
+                             void *v_cache, float *k_scale, float *v_scale, int32_t block_size, int64_t num_blocks,
+                             int64_t cache_block_stride, int64_t cache_tok_stride, int64_t cache_head_stride, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * mrope_decode_kv8 -- mrope_decode for the 8-bit cache: one new token a sequence, rotated at plane
+ * pos[s] - amount[s] and written at position pos[s] of the sequence (a negative pos: Q is rotated and
+ * nothing written).  v is required.
+ * ------------------------------------------------------------------------------------------- */
+mrope_status mrope_decode_kv8(void *q, int64_t q_tok_stride, int64_t q_head_stride, int32_t n_q_heads, const void *k,
+                              int64_t k_tok_stride, int64_t k_head_stride, int32_t n_kv_heads, const void *v,
+                              int64_t v_tok_stride, int64_t v_head_stride, int32_t n_seqs, const int32_t *pos,
+                              const int32_t *amount, const int32_t *block_tables, int64_t table_stride,
+                              int32_t table_width, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                              int32_t block_size, int64_t num_blocks, int64_t cache_block_stride, int64_t cache_tok_stride,
+                              int64_t cache_head_stride, int32_t head_dim, int32_t rot_dim, int32_t dtype, double theta,
+                              void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * mrope_attend_kv8 -- causal attention of packed query tokens over the 8-bit cache.
+ *
+ * q          rotated Q heads [n_tokens], strides as in mrope_apply; read only.  Query head h reads KV
+ *            head h / (n_q_heads / n_kv_heads); n_q_heads a multiple of n_kv_heads.
+ * cu_seqlens [n_seqs + 1] int32: the query tokens of each sequence; NULL: one token a sequence
+ *            (n_tokens == n_seqs).  Tokens behind cu_seqlens[n_seqs]: out and lse are left as they are.
+ * context_lens [n_seqs] int32: positions of each sequence in the cache, its query tokens included
+ *            (they are the last ones).  Query token i of len sees the positions j <= context - len + i
+ *            that its table holds.
+ * softmax_scale  the scores' factor (1/sqrt(head_dim) as a rule).
+ * out        [n_tokens] heads of `dtype` (may not overlap q): sum_j p_j v_j / sum_j p_j.  A row that
+ *            sees nothing is 0.
+ * lse        nullable, [n_tokens][n_q_heads] fp32: ln sum_j exp(score_j); -infinity for a row that
+ *            sees nothing.
+ * Precision: scores and sums in fp32; queries are not rounded (16-bit types) or kept to 2^-24
+ *            (fp32); probabilities are kept to 2^-16 (16-bit types) or 2^-24 (fp32) of their size.
+ *            What a row does not see reaches it in no way, NaN codes among it.
+ * workspace  256-byte aligned device memory of mrope_attend_kv8_workspace_bytes(...) bytes (0: may be
+ *            NULL), needing no initialisation; calls that share one must be ordered.
+ *            one_token: whether cu_seqlens is NULL.
+ * ------------------------------------------------------------------------------------------- */
+size_t mrope_attend_kv8_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                        int32_t head_dim, int32_t dtype, int32_t one_token, int32_t table_width,
+                                        int32_t block_size);
+mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_head_stride, int32_t n_q_heads,
+                              int64_t n_tokens, int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                              const int32_t *cu_seqlens, int32_t n_seqs, const int32_t *context_lens,
+                              const int32_t *block_tables, int64_t table_stride, int32_t table_width, const void *k_cache,
+                              const void *v_cache, const float *k_scale, const float *v_scale, int32_t block_size,
+                              int64_t num_blocks, int64_t cache_block_stride, int64_t cache_tok_stride,
+                              int64_t cache_head_stride, double softmax_scale, void *out, int64_t out_tok_stride,
+                              int64_t out_head_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Pages of the paged caches: growing, freeing, forking, compacting, copying.
+ *
+ * The state, all on the device and owned by the caller:
+ *   refcount      [num_blocks] int32: rows that hold the page; 0 = free
+ *   block_tables  [n_rows] rows of table_width int32 at table_stride: the pages of each row (sequence)
+ *                 in order, -1 = none
+ *   seq_lens      [n_rows] int32: positions the row has pages for (0 = an empty row)
+ * A new state is all 0, -1 and 0.  Pages are handed out lowest index first, so what a call leaves
+ * depends on the state it found and on nothing else.  The calls work for caches of every type: a
+ * `mrope_pool` is any tensor with one entry a page (K, V and their scales, of any number of layers).
+ *
+ * Requests that cannot be met change nothing and are reported per request in `status`:
+ * MROPE_PAGES_NOT_ENOUGH (this and every earlier request together want more pages than are free) or
+ * MROPE_PAGES_BAD_ROW (a row outside [0, n_rows), a row that an earlier request of the call names, a
+ * length below 0 or past the table; fork: a destination that is not empty).
+ *
+ * workspace  256-byte aligned, mrope_pages_workspace_bytes(num_blocks, n_rows) bytes, needing no
+ *            initialisation; calls that share one, or share the state, must be ordered.
+ * Limits: num_blocks <= 2^24, n_rows <= 2^22, at most n_rows requests a call.
+ * ------------------------------------------------------------------------------------------- */
+#define MROPE_MAX_POOLS 64
+#define MROPE_PAGES_NOT_ENOUGH 1
+#define MROPE_PAGES_BAD_ROW 2
+
+typedef struct {
+    void *ptr;            /* page 0 */
+    int64_t page_bytes;   /* contiguous bytes of a page */
+    int64_t page_stride;  /* bytes from a page to the next, >= page_bytes */
+} mrope_pool;
+
+size_t mrope_pages_workspace_bytes(int64_t num_blocks, int64_t n_rows);
+
+/* Gives each row rows[i] pages for new_lens[i] positions, in order of i, and sets its length (a row
+ * that has them already keeps its pages and its length).  The new pages' count is 1. */
+mrope_status mrope_pages_grow(int32_t *refcount, int64_t num_blocks, int32_t *block_tables, int64_t table_stride,
+                              int32_t table_width, int32_t *seq_lens, int64_t n_rows, int32_t block_size,
+                              const int32_t *rows, const int32_t *new_lens, int32_t n, int32_t *status, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Empties the rows: every page of a row loses one count, the row's table becomes -1 and its length 0.
+ * Rows outside [0, n_rows) are ignored; a row named twice is freed once. */
+mrope_status mrope_pages_free(int32_t *refcount, int64_t num_blocks, int32_t *block_tables, int64_t table_stride,
+                              int32_t table_width, int32_t *seq_lens, int64_t n_rows, const int32_t *rows, int32_t n,
+                              void *stream);
+
+/* Makes the empty row dst[i] a copy of row src[i] (as it was before the call; one row may be forked
+ * many times): the pages that src fills are shared, their counts go up by one, and a last page that is
+ * filled in part gets a page of its own with that page's contents in every pool, so both rows can be
+ * appended to. */
+mrope_status mrope_pages_fork(int32_t *refcount, int64_t num_blocks, int32_t *block_tables, int64_t table_stride,
+                              int32_t table_width, int32_t *seq_lens, int64_t n_rows, int32_t block_size,
+                              const int32_t *src, const int32_t *dst, int32_t n, int32_t *status,
+                              const mrope_pool *pools, int32_t n_pools, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/* Moves the live pages to the lowest indexes: with L pages live, the i-th free page below L takes the
+ * i-th live page from L on (contents in every pool, count and table entries).  moved [1] int32 out:
+ * how many.  The pages from L on are free afterwards, their contents as they were. */
+mrope_status mrope_pages_compact(int32_t *refcount, int64_t num_blocks, int32_t *block_tables, int64_t table_stride,
+                                 int32_t table_width, int32_t *seq_lens, int64_t n_rows, int32_t *moved,
+                                 const mrope_pool *pools, int32_t n_pools, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* Copies page src[i] to page dst[i] in every pool, i < n (device arrays).  Pairs with an index outside
+ * [0, num_blocks) are skipped.  A page may be the source of many pairs, but the destination of one
+ * only, and no page may be both: which of such copies is seen is undefined. */
+mrope_status mrope_pages_copy(const mrope_pool *pools, int32_t n_pools, int64_t num_blocks, const int32_t *src,
+                              const int32_t *dst, int32_t n, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
