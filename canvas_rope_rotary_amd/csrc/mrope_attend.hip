@@ -68,8 +68,19 @@ __device__ __forceinline__ bool find_tile(const Attend &a, int g, int64_t w, int
     return true;
 }
 
-// Positions that the row sees: [0, row_limit), <= 0 for none.
-__device__ __forceinline__ int64_t row_limit(const Tile &t, int g, int row) { return min(t.seen, t.past + row / g + 1); }
+// Positions that the row sees: [0, row_limit), 0 for none (at most 2^27: a table holds no more).
+__device__ __forceinline__ int32_t row_limit(const Tile &t, int g, int row)
+{
+    return (int32_t)max(min(t.seen, t.past + row / g + 1), (int64_t)0);
+}
+
+// A tile's context is cut into chunks of this many tokens: as near to n_chunks equal parts as multiples
+// of `unit` allow.
+__device__ __forceinline__ int32_t chunk_of(int32_t lim, int n_chunks, int unit)
+{
+    const int32_t c = (max(lim, 1) + n_chunks - 1) / n_chunks;
+    return (c + unit - 1) / unit * unit;
+}
 
 // ------------------------------------------------------------------ few rows -------------------
 // One workgroup: R rows against a chunk of the context, its four waves taking 32 tokens in turn.
@@ -91,8 +102,8 @@ __device__ __forceinline__ int64_t row_limit(const Tile &t, int g, int row) { re
 template <int NT>
 constexpr int kRowsOf = NT == 2 ? 8 : 4;
 constexpr int kFewWaves = 4;
-constexpr int kMinChunk = 128;   // a block of 32 tokens a wave
-constexpr int kMaxChunk = 4096;  // a lane keeps the page of one 16-token half block
+constexpr int kFewUnit = 128;    // a block of 32 tokens a wave
+constexpr int kFewMost = 4096;   // tokens of a chunk: a lane keeps the page of one 16-token half block
 
 __device__ __forceinline__ float row_ror8(float x)
 {
@@ -169,7 +180,7 @@ __device__ __forceinline__ void store_out8(const Attend &a, int64_t off, const f
 }
 
 template <int IO, int D, int NT>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a, int chunk, int n_chunks)
+__global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a, int n_chunks)
 {
     constexpr int R = kRowsOf<NT>;
     constexpr int NK = D / 64;   // 16-byte pieces of a key a lane holds
@@ -182,11 +193,11 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
     Tile tl;
     if (!find_tile<R>(a, g, blockIdx.x, lane, tl)) return;
     const int n_rows = min(R, tl.rows - tl.row0);
-    const int64_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);  // the most that a row of the tile sees
-    const int64_t lim_first = row_limit(tl, g, tl.row0);
-    const int64_t c0 = (int64_t)z * chunk;
+    const int32_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);  // the most that a row of the tile sees
+    const int32_t lim_first = row_limit(tl, g, tl.row0);
+    const int32_t chunk = chunk_of(lim_last, n_chunks, kFewUnit), c0 = z * chunk;
     if (z > 0 && c0 >= lim_last) return;
-    const int64_t c1 = min(c0 + chunk, lim_last);
+    const int32_t c1 = min(c0 + chunk, lim_last);
 
     // pages of this wave's half blocks, a lane each
     const int32_t *table = a.kv.tables + tl.s * kv.table_stride;
@@ -194,7 +205,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
     float ks = 1.0f, vs = 1.0f;
     bool valid = false;
     {
-        const int64_t tok = c0 + ((lane >> 1) * kFewWaves + wave) * 32 + (lane & 1) * 16;
+        const int32_t tok = c0 + ((lane >> 1) * kFewWaves + wave) * 32 + (lane & 1) * 16;
         if (tok < c1) {
             const int32_t page = table[tok >> kv.bs_shift];
             valid = page >= 0 && page < kv.num_blocks;
@@ -212,7 +223,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
     const int t = col / R, r = col % R;
     const bool live = t < NT && r < n_rows;
     const int row = tl.row0 + min(r, n_rows - 1);
-    const int64_t lim = row_limit(tl, g, row);
+    const int32_t lim = row_limit(tl, g, row);
     bf16x8 qf[2 * NK];
     {
         const int64_t off = (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head;
@@ -262,7 +273,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
         load_v(0);
     }
     for (int it = 0; it < n_mine; ++it) {
-        const int64_t tok0 = c0 + (int64_t)(it * kFewWaves + wave) * 32;
+        const int32_t tok0 = c0 + (it * kFewWaves + wave) * 32;
         const float ks0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks), 2 * it));
         const float ks1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks), 2 * it + 1));
         const float kscale = col < 8 ? ks0 : ks1;
@@ -290,7 +301,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
         }
         const bool ragged = tok0 + 32 > lim_first || !ok0 || !ok1;  // wave-uniform
         const bool ok = grp < 2 ? ok0 : ok1;
-        const int64_t mine0 = tok0 + 8 * grp;
+        const int32_t mine0 = tok0 + 8 * grp;
         if (ragged) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -409,7 +420,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
         sml[wave][r][1] = l;
     }
     __syncthreads();
-    const bool whole = n_chunks == 1 || lim_last <= chunk;
+    const bool whole = lim_last <= chunk;
     Partial<D, R> *part = static_cast<Partial<D, R> *>(a.workspace) +
                           (((int64_t)blockIdx.x * kv.nk + kvh) * n_chunks + z);
     for (int e = threadIdx.x; e < n_rows * (D / 8); e += 64 * kFewWaves) {
@@ -445,15 +456,464 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
     }
 }
 
+// ------------------------------------------------------------------ many rows ------------------
+// One workgroup: 128 rows (32 a wave) against the context, 64 tokens at a time through LDS.
+//
+// S^T = K Q^T runs in 16 bits (32 x 32 x 16): the codes of K are exact in bf16 and fp16, so the queries'
+// own type is exact too and fp32 queries take three bf16 terms (each the nearest to what the terms before
+// it leave).  K is decoded once, on its way to LDS; its page scale joins the softmax's factor.  (The
+// 8-bit instruction would take K as it lies, but sums a product's 64 terms with some 13 bits below the
+// largest: measured, the scores' sums then were off by 1e-6 of themselves where 32 bits give 4e-8.)
+//
+// O^T = V^T P^T runs on the 8-bit instruction (32 x 32 x 64, twice the 16-bit rate) for the 16-bit types,
+// with V's codes as they lie and P as N e4m3 terms, each 2^4 finer than the last: two keep P to 2^-8
+// (bf16's own rounding) at the price of one bf16 product, three keep fp16's.  V's page scale multiplies
+// P, and a tile's probabilities of a row are written under the power of two of the largest of them (the
+// instruction's block scale), so a row that lives on small pages, or far below its running maximum,
+// keeps its precision.  fp32 takes three bf16 terms of P and decodes V's operands.
+//
+// As in the kernel for few rows S^T leaves a lane with the scores of one row, here for 32 of the 64 keys,
+// and O^T takes them from there: key 32t + 8a + 4h + b is byte 16t + 4a + b of lane half h.  V goes to
+// LDS transposed in that order, four keys of a dim in a word; its 16-byte pieces are swapped by
+// (dim / 2) % 4 and 64 bytes left free every D/16 dims, which keeps the eight lanes of a read cycle and
+// the lanes of a write in different banks.  K's rows are 16 bytes longer for the same reason.
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kManyWaves = 4;
+constexpr int kManyRows = 32 * kManyWaves;
+constexpr int kManyUnit = 64;  // tokens of a tile
+
+__device__ __forceinline__ f32x16 mfma8(i32x8 x, i32x8 y, f32x16 c, int sx, int sy)
+{
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 0, 0, 0, sx, 0, sy);
+}
+
+// A product in 16 bits: fp16 for fp16 queries, else bf16.
+template <int IO>
+__device__ __forceinline__ f32x16 mfma16(u32x4 x, u32x4 y, f32x16 c)
+{
+    if constexpr (IO == kIoF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+}
+
+// Four e4m3 bytes as two words of the 16-bit type (exact).
+template <int IO>
+__device__ __forceinline__ uint2 decode4(uint32_t u)
+{
+    if constexpr (IO == kIoF16)
+        return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, false)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, true)));
+    else
+        return make_uint2(bf16_pair<false>(u, 1.0f), bf16_pair<true>(u, 1.0f));
+}
+
+// Four values to N terms of four codes each.
+template <int N>
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&t)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        t[i] = pack_e4m3(a, b, c, d);
+        if (i + 1 < N) {
+            const kv8_f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)t[i], false);
+            const kv8_f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)t[i], true);
+            a = (a - lo[0]) * 16.0f;
+            b = (b - lo[1]) * 16.0f;
+            c = (c - hi[0]) * 16.0f;
+            d = (d - hi[1]) * 16.0f;
+        }
+    }
+}
+
+template <int D>
+constexpr int kVB = D / 16;  // dims of V a thread transposes, for four keys
+
+template <int D>
+struct ManyTile {
+    uint8_t k[64][2 * D + 16];   // 16-bit keys
+    uint32_t v[16 * (D + 16)];   // word of (dim d, keys 4w..): see vword()
+    uint8_t nanv[16][D];         // bit b of [w][d]: key 4w + b has a NaN in dim d (written where a row may not see it)
+    float ks[4];                 // K's scale, by 16 keys
+    int32_t vexp[4];             // exponent of V's scale
+    int32_t live[4];             // whether those 16 keys have a page
+    int32_t nan;                 // 1 + the last tile in which `nanv` has a bit
+};
+
+template <int D>
+__device__ __forceinline__ int vword(int d, int piece)
+{
+    return 16 * d + 16 * (d / kVB<D>) + 4 * (piece ^ ((d >> 1) & 3));
+}
+
+__device__ __forceinline__ int32_t pick(const int32_t (&x)[4], int i)
+{
+    return i == 0 ? x[0] : (i == 1 ? x[1] : (i == 2 ? x[2] : x[3]));
+}
+
+__device__ __forceinline__ i32x8 join8(u32x4 x, u32x4 y)
+{
+    return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+}
+
+template <int IO, int D>
+__global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, int n_chunks)
+{
+    constexpr int QT = IO == kIoF32 ? 3 : 1;                          // 16-bit terms of Q
+    constexpr int N = IO == kIoBF16 ? 2 : 3;                          // terms of P: e4m3, or bf16 for fp32
+    constexpr int NS = D / 16, NO = D / 32;
+    constexpr int KL = D / 16;             // lanes that load a key row
+    constexpr int KR = 64 * kManyWaves / KL, KP = 64 / KR;  // key rows of a pass, passes
+    constexpr int VB = kVB<D>;
+    const Kv8 &kv = a.kv;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int col = lane & 31, half = lane >> 5;
+    const int g = a.nq / kv.nk, kvh = blockIdx.y, z = blockIdx.z;
+
+    Tile tl;
+    if (!find_tile<kManyRows>(a, g, blockIdx.x, lane, tl)) return;
+    const int n_rows = min(kManyRows, tl.rows - tl.row0);
+    const int32_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);
+    const int32_t chunk = chunk_of(lim_last, n_chunks, kManyUnit), c0 = z * chunk;
+    if (z > 0 && c0 >= lim_last) return;
+    const int32_t c1 = min(c0 + chunk, lim_last);
+    const int n_tiles = c1 > c0 ? (c1 - c0 + 63) / 64 : 0;
+
+    __shared__ ManyTile<D> tile[2];
+    __shared__ uint32_t bad[kManyRows][NO];  // bit d of a row: it saw a NaN in that dim of V
+
+    // this lane's row, and what the wave's rows see
+    const int r = wave * 32 + col;
+    const bool live = r < n_rows;
+    const int row = tl.row0 + min(r, n_rows - 1);
+    const int32_t lim = row_limit(tl, g, row);
+    const int32_t wfirst = row_limit(tl, g, tl.row0 + min(wave * 32, n_rows - 1));
+    const int32_t wlim = wave * 32 < n_rows ? row_limit(tl, g, tl.row0 + min(wave * 32 + 31, n_rows - 1)) : 0;
+    const int32_t first = row_limit(tl, g, tl.row0);  // every row sees the positions before this
+
+    // the scores' factor: its sign goes to Q, and zero makes Q zero, so the largest score is the largest sum
+    const float factor = a.scale_log2 != 0.0f ? __builtin_fabsf(a.scale_log2) : 1.0f;
+    const float sign = a.scale_log2 < 0.0f ? -1.0f : (a.scale_log2 > 0.0f ? 1.0f : 0.0f);
+
+    // Q: dims 16*s + 8*half .. + 7 of the lane's row
+    u32x4 qf[QT][NS];
+    {
+        const int64_t off = (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head + half * 8;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            float x[8];
+            unpack8<IO>(load8<IO>(a.q, off + s * 16), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= sign;
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = pack16x2<IO == kIoF16 ? kIoF16 : kIoBF16>(x[2 * i], x[2 * i + 1]);
+                    qf[t][s][i] = w;
+                    if (t + 1 < QT) {
+                        float lo, hi;
+                        unpack16x2<kIoBF16>(w, lo, hi);
+                        x[2 * i] -= lo;
+                        x[2 * i + 1] -= hi;
+                    }
+                }
+        }
+    }
+
+    // staging: this thread's pieces of a tile
+    const int32_t *table = kv.tables + tl.s * kv.table_stride;
+    u32x4 kreg[KP];
+    VRow<D> vreg[4];
+    const int kr = tid / KL, kc = tid % KL * 16;            // key rows kr, kr + KR, ...
+    const int vt = lane & 15, vc = (lane >> 4) + 4 * wave;  // keys 4*vt.., dims VB*vc..
+    int32_t pages[4];
+    float sc = 1.0f;
+    auto load_tile = [&](int i) {
+        const int32_t t0 = c0 + i * 64;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int32_t tok = t0 + 16 * j;
+            const int32_t page = table[min(tok, c1 - 1) >> kv.bs_shift];
+            pages[j] = tok < c1 && page >= 0 && page < kv.num_blocks ? page : -1;
+        }
+        auto at = [&](int k) {  // key k of the tile (a key without a page reads page 0)
+            return max(pick(pages, k >> 4), 0) * kv.c_block + ((t0 + k) & (kv.block_size - 1)) * kv.c_tok + kvh * kv.c_head;
+        };
+#pragma unroll
+        for (int p = 0; p < KP; ++p) kreg[p] = *reinterpret_cast<const u32x4 *>(kv.k + at(kr + p * KR) + kc);
+        const int64_t vb = at(4 * vt) + vc * VB;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vreg[j] = load_vrow<D>(kv.v + vb + j * kv.c_tok);
+        if (tid < 8) sc = (tid < 4 ? kv.k_scale : kv.v_scale)[(int64_t)max(pick(pages, tid & 3), 0) * kv.nk + kvh];
+    };
+    auto store_tile = [&](int i) {
+        ManyTile<D> &t = tile[i & 1];
+        const int32_t t0 = c0 + i * 64;
+#pragma unroll
+        for (int p = 0; p < KP; ++p)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint2 x = decode4<IO>(kreg[p][2 * h]), y = decode4<IO>(kreg[p][2 * h + 1]);
+                *reinterpret_cast<u32x4 *>(&t.k[kr + p * KR][2 * kc + 16 * h]) = u32x4{x.x, x.y, y.x, y.y};
+            }
+        if (t0 + 64 > first || (pages[0] | pages[1] | pages[2] | pages[3]) < 0) {
+            // what no row sees may hold anything: it must not reach the product; and where some rows see
+            // a NaN and others do not, the product goes on without it and the rows are told
+            const int32_t page = pick(pages, vt >> 2);
+            bool nan = false;
+#pragma unroll
+            for (int w = 0; w < VB / 4; ++w) {
+                uint32_t bits = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t x = vreg[j].w[w];
+                    if (page < 0 || t0 + 4 * vt + j >= lim_last) x = 0;
+                    const uint32_t n = (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in a NaN's byte
+                    bits |= n << j;
+                    vreg[j].w[w] = x & ~(n * 0xffu);
+                }
+                *reinterpret_cast<uint32_t *>(&t.nanv[vt][vc * VB + 4 * w]) = bits;
+                nan |= bits != 0;
+            }
+            if (nan) t.nan = i + 1;
+        }
+        // keys 4*vt..: tile half vt/8, eight-key group (vt/2)%4, lane half vt%2
+        const int piece = (vt & 1) * 2 + (vt >> 3), in = (vt >> 1) & 3;
+#pragma unroll
+        for (int w = 0; w < VB / 4; ++w) {
+            const uint32_t a0 = __builtin_amdgcn_perm(vreg[1].w[w], vreg[0].w[w], 0x05010400u), a1 = __builtin_amdgcn_perm(vreg[3].w[w], vreg[2].w[w], 0x05010400u);
+            const uint32_t b0 = __builtin_amdgcn_perm(vreg[1].w[w], vreg[0].w[w], 0x07030602u), b1 = __builtin_amdgcn_perm(vreg[3].w[w], vreg[2].w[w], 0x07030602u);
+            const int d = vc * VB + 4 * w;
+            t.v[vword<D>(d, piece) + in] = __builtin_amdgcn_perm(a1, a0, 0x05040100u);
+            t.v[vword<D>(d + 1, piece) + in] = __builtin_amdgcn_perm(a1, a0, 0x07060302u);
+            t.v[vword<D>(d + 2, piece) + in] = __builtin_amdgcn_perm(b1, b0, 0x05040100u);
+            t.v[vword<D>(d + 3, piece) + in] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+        }
+        if (tid < 4) {
+            t.ks[tid] = pow2(scale_exp_of(sc));
+            t.live[tid] = pick(pages, tid) >= 0;
+        } else if (tid < 8) {
+            t.vexp[tid - 4] = scale_exp_of(sc);
+        }
+    };
+
+    float m = kNoMax, l = 0.0f;
+    f32x16 o[NO];
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[i][q] = 0.0f;
+
+    if (tid < 2) tile[tid].nan = 0;
+    for (int i = tid; i < kManyRows * NO; i += 64 * kManyWaves) bad[i / NO][i % NO] = 0;
+    __syncthreads();
+    if (n_tiles > 0) {
+        load_tile(0);
+        store_tile(0);
+        if (n_tiles > 1) load_tile(1);
+    }
+    for (int it = 0; it < n_tiles; ++it) {
+        __syncthreads();  // tile `it` is in LDS; the other buffer's readers are done
+        const ManyTile<D> &t = tile[it & 1];
+        const int32_t t0 = c0 + it * 64;
+        if (it + 1 < n_tiles) {
+            store_tile(it + 1);
+            if (it + 2 < n_tiles) load_tile(it + 2);
+        }
+        if (t0 >= wlim) continue;  // none of the wave's rows sees the tile
+
+        f32x16 s[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) s[h][q] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NS; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 kf = *reinterpret_cast<const u32x4 *>(&t.k[32 * h + col][32 * k + 16 * half]);
+#pragma unroll
+                for (int n = 0; n < QT; ++n) s[h] = mfma16<IO>(kf, qf[n][k], s[h]);
+            }
+
+        // register 4a + b of s[h]: key 32h + 8a + 4*half + b
+        const bool all_live = (t.live[0] & t.live[1] & t.live[2] & t.live[3]) != 0;
+        if (t0 + 64 > wfirst || !all_live) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int key = 32 * h + 8 * (q >> 2) + 4 * half + (q & 3);
+                    if (t0 + key >= lim || !t.live[2 * h + (q >> 3)]) s[h][q] = -__builtin_inff();
+                }
+        }
+        float f[4], top[4];  // by 16 keys: the scores' factor, the largest score
+        int ev[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[j] = factor * t.ks[j];
+            ev[j] = t.vexp[j];
+            top[j] = s[j >> 1][8 * (j & 1)];
+#pragma unroll
+            for (int q = 1; q < 8; ++q) top[j] = fmaxf(top[j], s[j >> 1][8 * (j & 1) + q]);
+            top[j] *= f[j];
+        }
+        float hi = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        hi = fmaxf(hi, __shfl_xor(hi, 32));
+        const float m_new = fmaxf(m, hi);
+        if (__any(m_new > m)) {
+            const float c = __builtin_amdgcn_exp2f(m - m_new);
+            l *= c;
+#pragma unroll
+            for (int i = 0; i < NO; ++i) o[i] *= c;
+            m = m_new;
+        }
+        if constexpr (IO != kIoF32) {
+            float big = fmaxf(fmaxf(top[0] + (float)ev[0], top[1] + (float)ev[1]), fmaxf(top[2] + (float)ev[2], top[3] + (float)ev[3]));
+            big = fmaxf(big, __shfl_xor(big, 32));
+            const int pexp = (int)fminf(fmaxf(__builtin_ceilf(big - m), -90.0f), 121.0f);
+            uint32_t pf[N][8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float add = (float)(ev[j] - pexp + 8) - m;
+                float p[8], sum = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j >> 1][8 * (j & 1) + q], f[j], add));
+                    sum += p[q];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t w[N];
+                    split4<N>(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3], w);
+#pragma unroll
+                    for (int n = 0; n < N; ++n) pf[n][2 * j + e] = w[n];
+                }
+                l += __builtin_ldexpf(sum, pexp - 8 - ev[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < NO; ++i) {
+                const int d = 32 * i + col;
+                const i32x8 vf = join8(*reinterpret_cast<const u32x4 *>(&t.v[vword<D>(d, 2 * half)]),
+                                       *reinterpret_cast<const u32x4 *>(&t.v[vword<D>(d, 2 * half + 1)]));
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const i32x8 pb = {(int)pf[n][0], (int)pf[n][1], (int)pf[n][2], (int)pf[n][3],
+                                      (int)pf[n][4], (int)pf[n][5], (int)pf[n][6], (int)pf[n][7]};
+                    o[i] = mfma8(vf, pb, o[i], 127, 119 + pexp - 4 * n);
+                }
+            }
+        } else {
+            u32x4 pf[N][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float vs = pow2(ev[j]);
+                float p[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j >> 1][8 * (j & 1) + q], f[j], -m));
+                    l += p[q];
+                    p[q] *= vs;
+                }
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t w = pack16x2<kIoBF16>(p[2 * e], p[2 * e + 1]);
+                        float lo, hi2;
+                        unpack16x2<kIoBF16>(w, lo, hi2);
+                        p[2 * e] -= lo;
+                        p[2 * e + 1] -= hi2;
+                        pf[n][j][e] = w;
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < NO; ++i) {
+                const int d = 32 * i + col;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 x = *reinterpret_cast<const u32x4 *>(&t.v[vword<D>(d, 2 * half + h)]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint2 lo = decode4<IO>(x[2 * e]), hi2 = decode4<IO>(x[2 * e + 1]);
+#pragma unroll
+                        for (int n = 0; n < N; ++n) o[i] = mfma16<IO>(u32x4{lo.x, lo.y, hi2.x, hi2.y}, pf[n][2 * h + e], o[i]);
+                    }
+                }
+            }
+        }
+        if (t.nan == it + 1) {  // rare: the dims in which this lane's row sees a NaN, half of them a lane
+            const int32_t seen = lim - t0;
+#pragma unroll 1
+            for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d) {
+                uint32_t bad_d = 0;
+#pragma unroll 1
+                for (int w = 0; w < 16; ++w) bad_d |= t.nanv[w][d] & ((1u << min(max(seen - 4 * w, 0), 4)) - 1);
+                if (bad_d) bad[r][d >> 5] |= 1u << (d & 31);
+            }
+        }
+    }
+
+    l += __shfl_xor(l, 32);
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < NO; ++i) {
+        const uint32_t b = bad[r][i] >> (4 * half);  // both halves of a row's dims are marked by lanes of this wave
+        if (b)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                if ((b >> (8 * (q >> 2) + (q & 3))) & 1) o[i][q] = __builtin_nanf("");
+    }
+    const int64_t tok = tl.t0 + row / g;
+    const int head = kvh * g + row % g;
+    if (lim_last <= chunk) {
+        const float inv = 1.0f / l;
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float y[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) y[b] = l == 0.0f ? 0.0f : o[i][4 * e + b] * inv;
+                const int64_t at = tok * a.o_tok + head * a.o_head + 32 * i + 8 * e + 4 * half;
+                if constexpr (IO == kIoF32)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+                else
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+                        make_uint2(pack16x2<IO>(y[0], y[1]), pack16x2<IO>(y[2], y[3]));
+            }
+        if (a.lse && half == 0)
+            a.lse[tok * a.nq + head] = l == 0.0f ? -__builtin_inff() : 0.69314718055994531f * (m + __log2f(l));
+    } else {
+        Partial<D, kManyRows> *part = static_cast<Partial<D, kManyRows> *>(a.workspace) +
+                                      (((int64_t)blockIdx.x * kv.nk + kvh) * n_chunks + z);
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<float4 *>(&part->o[r][32 * i + 8 * e + 4 * half]) =
+                    make_float4(o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]);
+        if (half == 0) {
+            part->ml[r][0] = m;
+            part->ml[r][1] = l;
+        }
+    }
+}
+
 // Joins a tile's chunks: one workgroup a row, D/4 lanes over its dims and the rest over the chunks.
 template <int IO, int D, int R>
-__global__ __launch_bounds__(256) void attend_join_kernel(Attend a, int chunk, int n_chunks)
+__global__ __launch_bounds__(256) void attend_join_kernel(Attend a, int n_chunks, int unit)
 {
     const int g = a.nq / a.kv.nk, kvh = blockIdx.y, rr = blockIdx.z;
     Tile tl;
     if (!find_tile<R>(a, g, blockIdx.x, threadIdx.x & 63, tl)) return;
     const int n_rows = min(R, tl.rows - tl.row0);
-    const int64_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);
+    const int32_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);
+    const int32_t chunk = chunk_of(lim_last, n_chunks, unit);
     if (rr >= n_rows || lim_last <= chunk) return;
     const int n = (int)((lim_last + chunk - 1) / chunk);
     const Partial<D, R> *part = static_cast<const Partial<D, R> *>(a.workspace) +
@@ -503,28 +963,32 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Attend a, int chunk, i
 
 // ------------------------------------------------------------------ launchers ------------------
 struct Plan {
+    bool many;
     int64_t tiles;
-    int chunk, n_chunks;
-    size_t bytes;
+    int rows;      // of a tile
+    int n_chunks;
+    size_t bytes;  // of the workspace
 };
 
-// Chunks of the context: as many workgroups as fill the device several times over (kFill), no chunk
-// below 128 tokens (one block a wave) nor above 4,096 (the pages that a wave's lanes keep).
-constexpr int64_t kFill = 2048;
+// Tiles of many rows from this many rows a sequence and KV head on the average.
+constexpr int64_t kManyFrom = 16;
+// Workgroups wanted: the context is cut where the tiles alone are fewer.
+constexpr int64_t kFewFill = 2048, kManyFill = 512;
 
-Plan plan_few(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io, bool one_token,
-              int32_t table_width, int32_t block_size)
+Plan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io, bool one_token,
+               int32_t table_width, int32_t block_size)
 {
     Plan p{};
-    const int R = io == kIoF32 ? kRowsOf<3> : kRowsOf<2>;
-    const int g = nq / nk;
-    p.tiles = one_token ? (int64_t)n_seqs * ((g + R - 1) / R) : n_tokens * g / R + n_seqs;
-    const int64_t cap = std::max<int64_t>(1, (int64_t)table_width * block_size);
-    int64_t chunk = kMinChunk;
-    while (chunk < kMaxChunk && p.tiles * nk * ((cap + chunk - 1) / chunk) > kFill) chunk *= 2;
-    p.chunk = (int)chunk;
-    p.n_chunks = (int)((cap + chunk - 1) / chunk);
-    p.bytes = p.n_chunks > 1 ? (size_t)p.tiles * nk * p.n_chunks * (size_t)(R * (head_dim + 2) * 4) : 0;
+    const int64_t g = nq / nk, cap = std::max<int64_t>(1, (int64_t)table_width * block_size);
+    p.many = n_tokens * g > kManyFrom * n_seqs;
+    p.rows = p.many ? kManyRows : (io == kIoF32 ? kRowsOf<3> : kRowsOf<2>);
+    p.tiles = one_token ? (int64_t)n_seqs * ((g + p.rows - 1) / p.rows) : n_tokens * g / p.rows + n_seqs;
+    const int64_t unit = p.many ? kManyUnit : kFewUnit, fill = p.many ? kManyFill : kFewFill;
+    const int64_t most = (cap + unit - 1) / unit;
+    int64_t n = std::min(most, std::max<int64_t>(1, fill / (p.tiles * nk)));
+    if (!p.many) n = std::max(n, (cap + kFewMost - 1) / kFewMost);
+    p.n_chunks = (int)n;
+    p.bytes = n > 1 ? (size_t)(p.tiles * nk * n) * (size_t)(p.rows * (head_dim + 2) * 4) : 0;
     return p;
 }
 
@@ -532,11 +996,15 @@ template <int IO, int D>
 hipError_t launch_attend_d(const Attend &a, hipStream_t stream)
 {
     constexpr int NT = IO == kIoF32 ? 3 : 2;
-    const Plan p = plan_few(a.n_tokens, a.n_seqs, a.nq, a.kv.nk, D, IO, a.cu == nullptr, a.kv.table_width, a.kv.block_size);
-    attend_few_kernel<IO, D, NT><<<dim3((unsigned)p.tiles, a.kv.nk, p.n_chunks), 64 * kFewWaves, 0, stream>>>(a, p.chunk, p.n_chunks);
-    hipError_t e = hipGetLastError();
+    const Plan p = make_plan(a.n_tokens, a.n_seqs, a.nq, a.kv.nk, D, IO, a.cu == nullptr, a.kv.table_width, a.kv.block_size);
+    const dim3 grid((unsigned)p.tiles, a.kv.nk, p.n_chunks);
+    if (p.many) attend_many_kernel<IO, D><<<grid, 64 * kManyWaves, 0, stream>>>(a, p.n_chunks);
+    else attend_few_kernel<IO, D, NT><<<grid, 64 * kFewWaves, 0, stream>>>(a, p.n_chunks);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.n_chunks == 1) return e;
-    attend_join_kernel<IO, D, kRowsOf<NT>><<<dim3((unsigned)p.tiles, a.kv.nk, kRowsOf<NT>), 256, 0, stream>>>(a, p.chunk, p.n_chunks);
+    const dim3 join((unsigned)p.tiles, a.kv.nk, p.rows);
+    if (p.many) attend_join_kernel<IO, D, kManyRows><<<join, 256, 0, stream>>>(a, p.n_chunks, kManyUnit);
+    else attend_join_kernel<IO, D, kRowsOf<NT>><<<join, 256, 0, stream>>>(a, p.n_chunks, kFewUnit);
     return hipGetLastError();
 }
 
@@ -555,7 +1023,7 @@ hipError_t launch_attend_io(const Attend &a, hipStream_t stream)
 size_t attend_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io,
                               bool one_token, int32_t table_width, int32_t block_size)
 {
-    return plan_few(n_tokens, n_seqs, nq, nk, head_dim, io, one_token, table_width, block_size).bytes;
+    return make_plan(n_tokens, n_seqs, nq, nk, head_dim, io, one_token, table_width, block_size).bytes;
 }
 
 hipError_t launch_attend(const Attend &a, int io, hipStream_t stream)
