@@ -500,6 +500,11 @@ __device__ __forceinline__ f32x16 mfma16(u32x4 x, u32x4 y, f32x16 c)
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
 }
 
+// The output's sums stay in accumulation registers throughout: the compiler otherwise moved all of them
+// to the others and back in every tile, for the sake of a rescaling that few tiles do.
+__device__ __forceinline__ void keep_in_acc(f32x16 &x) { asm volatile("" : "+a"(x)); }
+__device__ __forceinline__ void keep_in_vec(f32x16 &x) { asm volatile("" : "+v"(x)); }
+
 // Four e4m3 bytes as two words of the 16-bit type (exact).
 template <int IO>
 __device__ __forceinline__ uint2 decode4(uint32_t u)
@@ -533,14 +538,18 @@ template <int D>
 constexpr int kVB = D / 16;  // dims of V a thread transposes, for four keys
 
 template <int D>
-struct ManyTile {
+struct alignas(16) ManyTile {
     uint8_t k[64][2 * D + 16];   // 16-bit keys
     uint32_t v[16 * (D + 16)];   // word of (dim d, keys 4w..): see vword()
     uint8_t nanv[16][D];         // bit b of [w][d]: key 4w + b has a NaN in dim d (written where a row may not see it)
-    float ks[4];                 // K's scale, by 16 keys
-    int32_t vexp[4];             // exponent of V's scale
-    int32_t live[4];             // whether those 16 keys have a page
     int32_t nan;                 // 1 + the last tile in which `nanv` has a bit
+};
+
+// What a tile's sixteens of keys share: their scales and whether they have a page.
+struct Sixteens {
+    float ks[4];    // K's scale
+    int32_t ev[4];  // exponent of V's scale
+    uint32_t live;  // bit j
 };
 
 template <int D>
@@ -549,9 +558,11 @@ __device__ __forceinline__ int vword(int d, int piece)
     return 16 * d + 16 * (d / kVB<D>) + 4 * (piece ^ ((d >> 1) & 3));
 }
 
-__device__ __forceinline__ int32_t pick(const int32_t (&x)[4], int i)
+// The larger of a lane's and its counterpart's in the other half of the wave.
+__device__ __forceinline__ float max_halves(float x)
 {
-    return i == 0 ? x[0] : (i == 1 ? x[1] : (i == 2 ? x[2] : x[3]));
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 __device__ __forceinline__ i32x8 join8(u32x4 x, u32x4 y)
@@ -574,7 +585,8 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     const int g = a.nq / kv.nk, kvh = blockIdx.y, z = blockIdx.z;
 
     Tile tl;
-    if (!find_tile<kManyRows>(a, g, blockIdx.x, lane, tl)) return;
+    const int64_t w = gridDim.x - 1 - blockIdx.x;  // a prompt's later tiles see more: they go first
+    if (!find_tile<kManyRows>(a, g, w, lane, tl)) return;
     const int n_rows = min(kManyRows, tl.rows - tl.row0);
     const int32_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);
     const int32_t chunk = chunk_of(lim_last, n_chunks, kManyUnit), c0 = z * chunk;
@@ -630,51 +642,81 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     VRow<D> vreg[4];
     const int kr = tid / KL, kc = tid % KL * 16;            // key rows kr, kr + KR, ...
     const int vt = lane & 15, vc = (lane >> 4) + 4 * wave;  // keys 4*vt.., dims VB*vc..
-    int32_t pages[4];
-    float sc = 1.0f;
-    auto load_tile = [&](int i) {
-        const int32_t t0 = c0 + i * 64;
+    const int bmask = kv.block_size - 1;                    // tiles begin at multiples of 64: a key's row in its page is its own
+    int64_t koff[KP];
+#pragma unroll
+    for (int p = 0; p < KP; ++p) koff[p] = ((kr + p * KR) & bmask) * kv.c_tok + kc + kvh * kv.c_head;
+    const int64_t voff = ((4 * vt) & bmask) * kv.c_tok + vc * VB + kvh * kv.c_head;
+
+    // Pages and scales of 16 tiles, a sixteen of keys a lane; those of the next 16 are fetched on the way.
+    struct Lanes {
+        int32_t page;  // -1 = none
+        float ks;
+        int32_t ev;
+    };
+    auto fetch_pages = [&](int group) {
+        const int32_t tok = c0 + (group * 64 + lane) * 16;
+        int32_t page = -1;
+        if (tok < c1) page = table[tok >> kv.bs_shift];
+        return page >= 0 && page < kv.num_blocks ? page : -1;
+    };
+    auto fetch_scales = [&](int32_t page) {
+        Lanes x{page, 1.0f, 0};
+        if (page >= 0) {
+            x.ks = kv.k_scale[(int64_t)page * kv.nk + kvh];
+            x.ev = scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]);
+        }
+        return x;
+    };
+    Lanes here{-1, 1.0f, 0}, ahead{-1, 1.0f, 0};
+    auto load_tile = [&](int i) {  // in order: 0, 1, 2, ...
+        const int at = (i & 15) * 4;
+        if (at == 0) here = i ? ahead : fetch_scales(fetch_pages(0));
+        if (at == 16) ahead.page = fetch_pages((i >> 4) + 1);
+        if (at == 32) ahead = fetch_scales(ahead.page);
+        Sixteens x;
+        x.live = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int32_t tok = t0 + 16 * j;
-            const int32_t page = table[min(tok, c1 - 1) >> kv.bs_shift];
-            pages[j] = tok < c1 && page >= 0 && page < kv.num_blocks ? page : -1;
+            x.ks[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(here.ks), at + j));
+            x.ev[j] = __builtin_amdgcn_readlane(here.ev, at + j);
+            x.live |= __builtin_amdgcn_readlane(here.page, at + j) >= 0 ? 1u << j : 0u;
         }
-        auto at = [&](int k) {  // key k of the tile (a key without a page reads page 0)
-            return max(pick(pages, k >> 4), 0) * kv.c_block + ((t0 + k) & (kv.block_size - 1)) * kv.c_tok + kvh * kv.c_head;
-        };
+        // (a key without a page reads page 0)
 #pragma unroll
-        for (int p = 0; p < KP; ++p) kreg[p] = *reinterpret_cast<const u32x4 *>(kv.k + at(kr + p * KR) + kc);
-        const int64_t vb = at(4 * vt) + vc * VB;
+        for (int p = 0; p < KP; ++p)
+            kreg[p] = *reinterpret_cast<const u32x4 *>(kv.k + max(__shfl(here.page, at + ((kr + p * KR) >> 4)), 0) * kv.c_block + koff[p]);
+        const uint8_t *pv = kv.v + max(__shfl(here.page, at + (vt >> 2)), 0) * kv.c_block + voff;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) vreg[j] = load_vrow<D>(kv.v + vb + j * kv.c_tok);
-        if (tid < 8) sc = (tid < 4 ? kv.k_scale : kv.v_scale)[(int64_t)max(pick(pages, tid & 3), 0) * kv.nk + kvh];
+        for (int j = 0; j < 4; ++j) vreg[j] = load_vrow<D>(pv + j * kv.c_tok);
+        return x;
     };
-    auto store_tile = [&](int i) {
+    auto store_tile = [&](int i, const Sixteens &x) {
         ManyTile<D> &t = tile[i & 1];
         const int32_t t0 = c0 + i * 64;
 #pragma unroll
         for (int p = 0; p < KP; ++p)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint2 x = decode4<IO>(kreg[p][2 * h]), y = decode4<IO>(kreg[p][2 * h + 1]);
-                *reinterpret_cast<u32x4 *>(&t.k[kr + p * KR][2 * kc + 16 * h]) = u32x4{x.x, x.y, y.x, y.y};
+                const uint2 lo = decode4<IO>(kreg[p][2 * h]), hi = decode4<IO>(kreg[p][2 * h + 1]);
+                *reinterpret_cast<u32x4 *>(&t.k[kr + p * KR][2 * kc + 16 * h]) = u32x4{lo.x, lo.y, hi.x, hi.y};
             }
-        if (t0 + 64 > first || (pages[0] | pages[1] | pages[2] | pages[3]) < 0) {
+        if (t0 + 64 > first || x.live != 15u) {
             // what no row sees may hold anything: it must not reach the product; and where some rows see
             // a NaN and others do not, the product goes on without it and the rows are told
-            const int32_t page = pick(pages, vt >> 2);
+            const bool has = (x.live >> (vt >> 2)) & 1;
             bool nan = false;
 #pragma unroll
             for (int w = 0; w < VB / 4; ++w) {
                 uint32_t bits = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    uint32_t x = vreg[j].w[w];
-                    if (page < 0 || t0 + 4 * vt + j >= lim_last) x = 0;
-                    const uint32_t n = (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in a NaN's byte
+                    uint32_t y = vreg[j].w[w];
+                    asm volatile("" : "+v"(y));  // not before the branch
+                    if (!has || t0 + 4 * vt + j >= lim_last) y = 0;
+                    const uint32_t n = (((y & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in a NaN's byte
                     bits |= n << j;
-                    vreg[j].w[w] = x & ~(n * 0xffu);
+                    vreg[j].w[w] = y & ~(n * 0xffu);
                 }
                 *reinterpret_cast<uint32_t *>(&t.nanv[vt][vc * VB + 4 * w]) = bits;
                 nan |= bits != 0;
@@ -693,12 +735,6 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
             t.v[vword<D>(d + 2, piece) + in] = __builtin_amdgcn_perm(b1, b0, 0x05040100u);
             t.v[vword<D>(d + 3, piece) + in] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
         }
-        if (tid < 4) {
-            t.ks[tid] = pow2(scale_exp_of(sc));
-            t.live[tid] = pick(pages, tid) >= 0;
-        } else if (tid < 8) {
-            t.vexp[tid - 4] = scale_exp_of(sc);
-        }
     };
 
     float m = kNoMax, l = 0.0f;
@@ -707,30 +743,41 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     for (int i = 0; i < NO; ++i)
 #pragma unroll
         for (int q = 0; q < 16; ++q) o[i][q] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NO; ++i) keep_in_acc(o[i]);
 
     if (tid < 2) tile[tid].nan = 0;
     for (int i = tid; i < kManyRows * NO; i += 64 * kManyWaves) bad[i / NO][i % NO] = 0;
     __syncthreads();
+    Sixteens cur{}, next{}, then{};
     if (n_tiles > 0) {
-        load_tile(0);
-        store_tile(0);
-        if (n_tiles > 1) load_tile(1);
+        cur = load_tile(0);
+        store_tile(0, cur);
+        if (n_tiles > 1) next = load_tile(1);
     }
-    for (int it = 0; it < n_tiles; ++it) {
+    // tiles that this wave's rows see, then those that it only helps to stage
+    const int n_mine = min(n_tiles, wlim > c0 ? (wlim - c0 + 63) / 64 : 0);
+    int it = 0;
+    auto stage = [&]() {
         __syncthreads();  // tile `it` is in LDS; the other buffer's readers are done
+        if (it + 1 < n_tiles) {
+            store_tile(it + 1, next);
+            if (it + 2 < n_tiles) then = load_tile(it + 2);
+        }
+    };
+    for (; it < n_mine; ++it, cur = next, next = then) {
+        stage();
         const ManyTile<D> &t = tile[it & 1];
         const int32_t t0 = c0 + it * 64;
-        if (it + 1 < n_tiles) {
-            store_tile(it + 1);
-            if (it + 2 < n_tiles) load_tile(it + 2);
-        }
-        if (t0 >= wlim) continue;  // none of the wave's rows sees the tile
 
         f32x16 s[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int q = 0; q < 16; ++q) s[h][q] = 0.0f;
+        keep_in_vec(s[0]);
+        keep_in_vec(s[1]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < NS; ++k)
 #pragma unroll
@@ -739,43 +786,56 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
 #pragma unroll
                 for (int n = 0; n < QT; ++n) s[h] = mfma16<IO>(kf, qf[n][k], s[h]);
             }
+        // operands are read two steps ahead of their products, no more: the registers are needed
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int k = 0; k < NS - 2; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 2 * QT, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 4 * QT, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        keep_in_vec(s[0]);
+        keep_in_vec(s[1]);
 
         // register 4a + b of s[h]: key 32h + 8a + 4*half + b
-        const bool all_live = (t.live[0] & t.live[1] & t.live[2] & t.live[3]) != 0;
-        if (t0 + 64 > wfirst || !all_live) {
+        if (t0 + 64 > wfirst || cur.live != 15u) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int key = 32 * h + 8 * (q >> 2) + 4 * half + (q & 3);
-                    if (t0 + key >= lim || !t.live[2 * h + (q >> 3)]) s[h][q] = -__builtin_inff();
+                    if (t0 + key >= lim || !((cur.live >> (2 * h + (q >> 3))) & 1)) s[h][q] = -__builtin_inff();
                 }
         }
         float f[4], top[4];  // by 16 keys: the scores' factor, the largest score
         int ev[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f[j] = factor * t.ks[j];
-            ev[j] = t.vexp[j];
+            f[j] = factor * cur.ks[j];
+            ev[j] = cur.ev[j];
             top[j] = s[j >> 1][8 * (j & 1)];
 #pragma unroll
             for (int q = 1; q < 8; ++q) top[j] = fmaxf(top[j], s[j >> 1][8 * (j & 1) + q]);
             top[j] *= f[j];
         }
         float hi = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        hi = fmaxf(hi, __shfl_xor(hi, 32));
-        const float m_new = fmaxf(m, hi);
-        if (__any(m_new > m)) {
+        const float m_new = fmaxf(m, max_halves(hi));
+        // the sums follow the maximum only where it has grown by 2^8: until then p exceeds 1 and nothing is lost
+        if (__any(m_new > m + 8.0f)) {
             const float c = __builtin_amdgcn_exp2f(m - m_new);
             l *= c;
 #pragma unroll
-            for (int i = 0; i < NO; ++i) o[i] *= c;
+            for (int i = 0; i < NO; ++i) {
+                keep_in_acc(o[i]);  // nor read before the branch
+                o[i] *= c;
+                keep_in_acc(o[i]);
+            }
             m = m_new;
         }
         if constexpr (IO != kIoF32) {
             float big = fmaxf(fmaxf(top[0] + (float)ev[0], top[1] + (float)ev[1]), fmaxf(top[2] + (float)ev[2], top[3] + (float)ev[3]));
-            big = fmaxf(big, __shfl_xor(big, 32));
-            const int pexp = (int)fminf(fmaxf(__builtin_ceilf(big - m), -90.0f), 121.0f);
+            const int pexp = (int)fminf(fmaxf(__builtin_ceilf(max_halves(big) - m), -90.0f), 121.0f);
             uint32_t pf[N][8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -846,6 +906,8 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < NO; ++i) keep_in_acc(o[i]);
         if (t.nan == it + 1) {  // rare: the dims in which this lane's row sees a NaN, half of them a lane
             const int32_t seen = lim - t0;
 #pragma unroll 1
@@ -857,6 +919,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
             }
         }
     }
+    for (; it < n_tiles; ++it, next = then) stage();
 
     l += __shfl_xor(l, 32);
     if (!live) return;
@@ -890,7 +953,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
             a.lse[tok * a.nq + head] = l == 0.0f ? -__builtin_inff() : 0.69314718055994531f * (m + __log2f(l));
     } else {
         Partial<D, kManyRows> *part = static_cast<Partial<D, kManyRows> *>(a.workspace) +
-                                      (((int64_t)blockIdx.x * kv.nk + kvh) * n_chunks + z);
+                                      ((w * kv.nk + kvh) * n_chunks + z);
 #pragma unroll
         for (int i = 0; i < NO; ++i)
 #pragma unroll
