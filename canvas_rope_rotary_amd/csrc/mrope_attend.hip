@@ -461,9 +461,10 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
 //
 // S^T = K Q^T runs in 16 bits (32 x 32 x 16): the codes of K are exact in bf16 and fp16, so the queries'
 // own type is exact too and fp32 queries take three bf16 terms (each the nearest to what the terms before
-// it leave).  K is decoded once, on its way to LDS; its page scale joins the softmax's factor.  (The
-// 8-bit instruction would take K as it lies, but sums a product's 64 terms with some 13 bits below the
-// largest: measured, the scores' sums then were off by 1e-6 of themselves where 32 bits give 4e-8.)
+// it leave).  K lies in LDS as it does in the cache and is decoded behind the matrix unit's back; its page
+// scale joins the softmax's factor.  (The 8-bit instruction would take K undecoded, but sums a product's
+// 64 terms with some 13 bits below the largest: measured, the scores' sums then were off by 1e-6 of
+// themselves where 32 bits give 4e-8.)
 //
 // O^T = V^T P^T runs on the 8-bit instruction (32 x 32 x 64, twice the 16-bit rate) for the 16-bit types,
 // with V's codes as they lie and P as N e4m3 terms, each 2^4 finer than the last: two keep P to 2^-8
@@ -503,17 +504,18 @@ __device__ __forceinline__ f32x16 mfma16(u32x4 x, u32x4 y, f32x16 c)
 // The output's sums stay in accumulation registers throughout: the compiler otherwise moved all of them
 // to the others and back in every tile, for the sake of a rescaling that few tiles do.
 __device__ __forceinline__ void keep_in_acc(f32x16 &x) { asm volatile("" : "+a"(x)); }
-__device__ __forceinline__ void keep_in_vec(f32x16 &x) { asm volatile("" : "+v"(x)); }
 
-// Four e4m3 bytes as two words of the 16-bit type (exact).
+// Eight e4m3 bytes in the 16-bit type (exact).
 template <int IO>
-__device__ __forceinline__ uint2 decode4(uint32_t u)
+__device__ __forceinline__ u32x4 decode8(uint32_t u, uint32_t v)
 {
     if constexpr (IO == kIoF16)
-        return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, false)),
-                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, true)));
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 1.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 1.0f, true))};
     else
-        return make_uint2(bf16_pair<false>(u, 1.0f), bf16_pair<true>(u, 1.0f));
+        return u32x4{bf16_pair<false>(u, 1.0f), bf16_pair<true>(u, 1.0f), bf16_pair<false>(v, 1.0f), bf16_pair<true>(v, 1.0f)};
 }
 
 // Four values to N terms of four codes each.
@@ -538,11 +540,12 @@ template <int D>
 constexpr int kVB = D / 16;  // dims of V a thread transposes, for four keys
 
 template <int D>
-struct alignas(16) ManyTile {
-    uint8_t k[64][2 * D + 16];   // 16-bit keys
-    uint32_t v[16 * (D + 16)];   // word of (dim d, keys 4w..): see vword()
-    uint8_t nanv[16][D];         // bit b of [w][d]: key 4w + b has a NaN in dim d (written where a row may not see it)
-    int32_t nan;                 // 1 + the last tile in which `nanv` has a bit
+struct alignas(16) ManyLds {
+    uint8_t k[2][64][D + 16];           // keys, as they lie in the cache
+    uint32_t v[3][16 * (D + 16)];       // word of (dim d, keys 4w..): see vword()
+    uint8_t nanv[2][16][D];             // bit b of [w][d]: key 4w + b has a NaN in dim d (written where a row may not see it)
+    uint32_t bad[kManyRows][D / 32];    // bit d of a row: it saw a NaN in that dim of V
+    int32_t nan[2];                     // 1 + the last tile in which `nanv` has a bit
 };
 
 // What a tile's sixteens of keys share: their scales and whether they have a page.
@@ -575,6 +578,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
 {
     constexpr int QT = IO == kIoF32 ? 3 : 1;                          // 16-bit terms of Q
     constexpr int N = IO == kIoBF16 ? 2 : 3;                          // terms of P: e4m3, or bf16 for fp32
+    constexpr int PW = IO == kIoF32 ? 4 : 2;                          // 16-byte words of a term of a lane's P
     constexpr int NS = D / 16, NO = D / 32;
     constexpr int KL = D / 16;             // lanes that load a key row
     constexpr int KR = 64 * kManyWaves / KL, KP = 64 / KR;  // key rows of a pass, passes
@@ -594,8 +598,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     const int32_t c1 = min(c0 + chunk, lim_last);
     const int n_tiles = c1 > c0 ? (c1 - c0 + 63) / 64 : 0;
 
-    __shared__ ManyTile<D> tile[2];
-    __shared__ uint32_t bad[kManyRows][NO];  // bit d of a row: it saw a NaN in that dim of V
+    __shared__ ManyLds<D> lds;
 
     // this lane's row, and what the wave's rows see
     const int r = wave * 32 + col;
@@ -610,14 +613,14 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     const float factor = a.scale_log2 != 0.0f ? __builtin_fabsf(a.scale_log2) : 1.0f;
     const float sign = a.scale_log2 < 0.0f ? -1.0f : (a.scale_log2 > 0.0f ? 1.0f : 0.0f);
 
-    // Q: dims 16*s + 8*half .. + 7 of the lane's row
+    // Q of the lane's row: step s takes dims 32*(s/2) + 16*half + 8*(s%2) .. + 7, as a 16-byte piece of K holds them
     u32x4 qf[QT][NS];
     {
-        const int64_t off = (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head + half * 8;
+        const int64_t off = (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head + half * 16;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             float x[8];
-            unpack8<IO>(load8<IO>(a.q, off + s * 16), x);
+            unpack8<IO>(load8<IO>(a.q, off + 32 * (s >> 1) + 8 * (s & 1)), x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] *= sign;
 #pragma unroll
@@ -669,11 +672,14 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
         return x;
     };
     Lanes here{-1, 1.0f, 0}, ahead{-1, 1.0f, 0};
-    auto load_tile = [&](int i) {  // in order: 0, 1, 2, ...
-        const int at = (i & 15) * 4;
+    auto turn_pages = [&](int i) {  // before load_tile(i), in order
+        const int at = i & 15;
         if (at == 0) here = i ? ahead : fetch_scales(fetch_pages(0));
-        if (at == 16) ahead.page = fetch_pages((i >> 4) + 1);
-        if (at == 32) ahead = fetch_scales(ahead.page);
+        if (at == 4) ahead.page = fetch_pages((i >> 4) + 1);
+        if (at == 8) ahead = fetch_scales(ahead.page);
+    };
+    auto load_tile = [&](int i) {
+        const int at = (i & 15) * 4;
         Sixteens x;
         x.live = 0;
 #pragma unroll
@@ -682,7 +688,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
             x.ev[j] = __builtin_amdgcn_readlane(here.ev, at + j);
             x.live |= __builtin_amdgcn_readlane(here.page, at + j) >= 0 ? 1u << j : 0u;
         }
-        // (a key without a page reads page 0)
+        // (a key without a page, or of a tile past the last, reads page 0)
 #pragma unroll
         for (int p = 0; p < KP; ++p)
             kreg[p] = *reinterpret_cast<const u32x4 *>(kv.k + max(__shfl(here.page, at + ((kr + p * KR) >> 4)), 0) * kv.c_block + koff[p]);
@@ -691,50 +697,49 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
         for (int j = 0; j < 4; ++j) vreg[j] = load_vrow<D>(pv + j * kv.c_tok);
         return x;
     };
-    auto store_tile = [&](int i, const Sixteens &x) {
-        ManyTile<D> &t = tile[i & 1];
+    // What no row sees may hold anything: it must not reach the product; and where some rows see a NaN and
+    // others do not, the product goes on without it and the rows are told.
+    auto clean_v = [&](int i, const Sixteens &x) {
         const int32_t t0 = c0 + i * 64;
-#pragma unroll
-        for (int p = 0; p < KP; ++p)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint2 lo = decode4<IO>(kreg[p][2 * h]), hi = decode4<IO>(kreg[p][2 * h + 1]);
-                *reinterpret_cast<u32x4 *>(&t.k[kr + p * KR][2 * kc + 16 * h]) = u32x4{lo.x, lo.y, hi.x, hi.y};
-            }
-        if (t0 + 64 > first || x.live != 15u) {
-            // what no row sees may hold anything: it must not reach the product; and where some rows see
-            // a NaN and others do not, the product goes on without it and the rows are told
-            const bool has = (x.live >> (vt >> 2)) & 1;
-            bool nan = false;
-#pragma unroll
-            for (int w = 0; w < VB / 4; ++w) {
-                uint32_t bits = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t y = vreg[j].w[w];
-                    asm volatile("" : "+v"(y));  // not before the branch
-                    if (!has || t0 + 4 * vt + j >= lim_last) y = 0;
-                    const uint32_t n = (((y & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in a NaN's byte
-                    bits |= n << j;
-                    vreg[j].w[w] = y & ~(n * 0xffu);
-                }
-                *reinterpret_cast<uint32_t *>(&t.nanv[vt][vc * VB + 4 * w]) = bits;
-                nan |= bits != 0;
-            }
-            if (nan) t.nan = i + 1;
-        }
-        // keys 4*vt..: tile half vt/8, eight-key group (vt/2)%4, lane half vt%2
-        const int piece = (vt & 1) * 2 + (vt >> 3), in = (vt >> 1) & 3;
+        if (t0 + 64 <= first && x.live == 15u) return;
+        const bool has = (x.live >> (vt >> 2)) & 1;
+        bool nan = false;
 #pragma unroll
         for (int w = 0; w < VB / 4; ++w) {
-            const uint32_t a0 = __builtin_amdgcn_perm(vreg[1].w[w], vreg[0].w[w], 0x05010400u), a1 = __builtin_amdgcn_perm(vreg[3].w[w], vreg[2].w[w], 0x05010400u);
-            const uint32_t b0 = __builtin_amdgcn_perm(vreg[1].w[w], vreg[0].w[w], 0x07030602u), b1 = __builtin_amdgcn_perm(vreg[3].w[w], vreg[2].w[w], 0x07030602u);
-            const int d = vc * VB + 4 * w;
-            t.v[vword<D>(d, piece) + in] = __builtin_amdgcn_perm(a1, a0, 0x05040100u);
-            t.v[vword<D>(d + 1, piece) + in] = __builtin_amdgcn_perm(a1, a0, 0x07060302u);
-            t.v[vword<D>(d + 2, piece) + in] = __builtin_amdgcn_perm(b1, b0, 0x05040100u);
-            t.v[vword<D>(d + 3, piece) + in] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+            uint32_t bits = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t y = vreg[j].w[w];
+                asm volatile("" : "+v"(y));  // not before the branch
+                if (!has || t0 + 4 * vt + j >= lim_last) y = 0;
+                const uint32_t n = (((y & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in a NaN's byte
+                bits |= n << j;
+                vreg[j].w[w] = y & ~(n * 0xffu);
+            }
+            *reinterpret_cast<uint32_t *>(&lds.nanv[i & 1][vt][vc * VB + 4 * w]) = bits;
+            nan |= bits != 0;
         }
+        if (nan) lds.nan[i & 1] = i + 1;
+    };
+    // keys 4*vt..: tile half vt/8, eight-key group (vt/2)%4, lane half vt%2; the swap of pieces takes four values
+    int vput[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) vput[e] = 16 * VB * vc + 16 * vc + 4 * (((vt & 1) * 2 + (vt >> 3)) ^ ((VB / 2 * vc + e) & 3)) + ((vt >> 1) & 3);
+    constexpr int kSlices = KP + VB / 4;
+    auto store_slice = [&](int n, int i, uint32_t *vbuf) {
+        if (n < KP) {
+            *reinterpret_cast<u32x4 *>(&lds.k[i & 1][kr][kc] + n * KR * (D + 16)) = kreg[n < KP ? n : 0];
+            return;
+        }
+        const int w = n - KP;
+        const uint32_t r0 = vreg[0].w[w], r1 = vreg[1].w[w], r2 = vreg[2].w[w], r3 = vreg[3].w[w];
+        const uint32_t a0 = __builtin_amdgcn_perm(r1, r0, 0x05010400u), a1 = __builtin_amdgcn_perm(r3, r2, 0x05010400u);
+        const uint32_t b0 = __builtin_amdgcn_perm(r1, r0, 0x07030602u), b1 = __builtin_amdgcn_perm(r3, r2, 0x07030602u);
+        uint32_t *p0 = vbuf + vput[(2 * w) & 3] + 64 * w, *p1 = vbuf + vput[(2 * w + 1) & 3] + 64 * w;
+        p0[0] = __builtin_amdgcn_perm(a1, a0, 0x05040100u);
+        p0[16] = __builtin_amdgcn_perm(a1, a0, 0x07060302u);
+        p1[32] = __builtin_amdgcn_perm(b1, b0, 0x05040100u);
+        p1[48] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
     };
 
     float m = kNoMax, l = 0.0f;
@@ -746,57 +751,112 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
 #pragma unroll
     for (int i = 0; i < NO; ++i) keep_in_acc(o[i]);
 
-    if (tid < 2) tile[tid].nan = 0;
-    for (int i = tid; i < kManyRows * NO; i += 64 * kManyWaves) bad[i / NO][i % NO] = 0;
+    // P of the tile before, in terms: its product with V is taken while the next softmax runs
+    u32x4 pf[N][PW];
+    int pexp = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < PW; ++e) pf[n][e] = u32x4{0, 0, 0, 0};
+    const int vget0 = vword<D>(col, 2 * half), vget1 = vword<D>(col, 2 * half + 1);
+    auto value_piece = [&](const uint32_t *vbuf, int i, int which) {
+        return *reinterpret_cast<const u32x4 *>(vbuf + (which ? vget1 : vget0) + (512 + 512 / VB) * i);
+    };
+    auto value_product = [&](int i, u32x4 x0, u32x4 x1) {
+        if constexpr (IO != kIoF32) {
+            const i32x8 vf = join8(x0, x1);
+#pragma unroll
+            for (int n = 0; n < N; ++n) o[i] = mfma8(vf, join8(pf[n][0], pf[n][1]), o[i], 127, 119 + pexp - 4 * n);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const u32x4 v = decode8<IO>((h ? x1 : x0)[2 * e], (h ? x1 : x0)[2 * e + 1]);
+#pragma unroll
+                    for (int n = 0; n < N; ++n) o[i] = mfma16<IO>(v, pf[n][2 * h + e], o[i]);
+                }
+        }
+    };
+
+    if (tid < 2) lds.nan[tid] = 0;
+    for (int i = tid; i < kManyRows * NO; i += 64 * kManyWaves) lds.bad[i / NO][i % NO] = 0;
+    for (int i = tid; i < 16 * (D + 16); i += 64 * kManyWaves) lds.v[2][i] = 0;  // before the first tile: nothing
     __syncthreads();
     Sixteens cur{}, next{}, then{};
     if (n_tiles > 0) {
+        turn_pages(0);
         cur = load_tile(0);
-        store_tile(0, cur);
-        if (n_tiles > 1) next = load_tile(1);
+        clean_v(0, cur);
+#pragma unroll
+        for (int n = 0; n < kSlices; ++n) store_slice(n, 0, lds.v[0]);
+        turn_pages(1);
+        next = load_tile(1);
     }
+    // V's buffers of tiles it - 1, it and it + 1
+    uint32_t *vprev = lds.v[2], *vcur = lds.v[0], *vnext = lds.v[1];
+    auto turn = [&]() {
+        uint32_t *x = vprev;
+        vprev = vcur;
+        vcur = vnext;
+        vnext = x;
+        cur = next;
+        next = then;
+    };
     // tiles that this wave's rows see, then those that it only helps to stage
     const int n_mine = min(n_tiles, wlim > c0 ? (wlim - c0 + 63) / 64 : 0);
     int it = 0;
-    auto stage = [&]() {
-        __syncthreads();  // tile `it` is in LDS; the other buffer's readers are done
-        if (it + 1 < n_tiles) {
-            store_tile(it + 1, next);
-            if (it + 2 < n_tiles) then = load_tile(it + 2);
-        }
-    };
-    for (; it < n_mine; ++it, cur = next, next = then) {
-        stage();
-        const ManyTile<D> &t = tile[it & 1];
+    for (; it < n_mine; ++it, turn()) {
         const int32_t t0 = c0 + it * 64;
+        __syncthreads();  // tile `it` is in LDS, and tiles it - 1 (K) and it - 2 (V) have been read
+        clean_v(it + 1, next);
+        turn_pages(it + 2);
+        __builtin_amdgcn_sched_barrier(0);
 
+        // The scores, step by step: a 16-byte piece of keys is two steps of the product.  Pieces are read
+        // kAhead steps before their use and decoded one before, while the matrix unit is busy; beside
+        // them the next tile goes to LDS, and the one after it is asked for.  (Past the last tile both are done for nobody.)
+        constexpr int NJ = NS, kAhead = NJ < 6 ? 2 : 6;
+        const uint8_t *kb = &lds.k[it & 1][col][16 * half];
+        auto key_piece = [&](int j) { return *reinterpret_cast<const u32x4 *>(kb + (j & 1) * 32 * (D + 16) + (j >> 1) * 32); };
         f32x16 s[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int q = 0; q < 16; ++q) s[h][q] = 0.0f;
-        keep_in_vec(s[0]);
-        keep_in_vec(s[1]);
-        __builtin_amdgcn_sched_barrier(0);
+        u32x4 piece[kAhead], ka[2], kn[2];
 #pragma unroll
-        for (int k = 0; k < NS; ++k)
+        for (int j = 0; j < kAhead; ++j) piece[j] = key_piece(j);
+        ka[0] = decode8<IO>(piece[0][0], piece[0][1]);
+        ka[1] = decode8<IO>(piece[0][2], piece[0][3]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u32x4 kf = *reinterpret_cast<const u32x4 *>(&t.k[32 * h + col][32 * k + 16 * half]);
+        for (int j = 0; j < NJ; ++j) {
+            if (j + kAhead < NJ) piece[j % kAhead] = key_piece(j + kAhead);
 #pragma unroll
-                for (int n = 0; n < QT; ++n) s[h] = mfma16<IO>(kf, qf[n][k], s[h]);
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int n = 0; n < QT; ++n) s[j & 1] = mfma16<IO>(ka[u], qf[n][(j & ~1) + u], s[j & 1]);
+            constexpr int kPer = (kSlices + NJ / 2 - 1) / (NJ / 2);
+#pragma unroll
+            for (int n = j * kPer; n < (j + 1) * kPer; ++n)
+                if (n < kSlices) store_slice(n, it + 1, vnext);
+            if (j == NJ / 2) then = load_tile(it + 2);
+            if (j + 1 < NJ) {
+                const u32x4 x = piece[(j + 1) % kAhead];
+                kn[0] = decode8<IO>(x[0], x[1]);
+                kn[1] = decode8<IO>(x[2], x[3]);
+                ka[0] = kn[0];
+                ka[1] = kn[1];
             }
-        // operands are read two steps ahead of their products, no more: the registers are needed
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-#pragma unroll
-        for (int k = 0; k < NS - 2; ++k) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 2 * QT, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, 4 * QT, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        keep_in_vec(s[0]);
-        keep_in_vec(s[1]);
+        const bool nan_here = lds.nan[it & 1] == it + 1;
+        u32x4 vx[3][2];  // V's operands, two products ahead
+#pragma unroll
+        for (int i = 0; i < 2 && i < NO; ++i) {
+            vx[i][0] = value_piece(vprev, i, 0);
+            vx[i][1] = value_piece(vprev, i, 1);
+        }
 
         // register 4a + b of s[h]: key 32h + 8a + 4*half + b
         if (t0 + 64 > wfirst || cur.live != 15u) {
@@ -808,21 +868,86 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
                     if (t0 + key >= lim || !((cur.live >> (2 * h + (q >> 3))) & 1)) s[h][q] = -__builtin_inff();
                 }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        // The softmax, and between its steps the tile before's product with V.
         float f[4], top[4];  // by 16 keys: the scores' factor, the largest score
-        int ev[4];
+        int ev[4], pexp_new = 0;
+        float m_new = m, m_top = m, ladd = 0.0f;
+        bool moves = false;
+        u32x4 pn[N][PW];
+        auto begin = [&]() {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[j] = factor * cur.ks[j];
-            ev[j] = cur.ev[j];
-            top[j] = s[j >> 1][8 * (j & 1)];
+            for (int j = 0; j < 4; ++j) {
+                f[j] = factor * cur.ks[j];
+                ev[j] = cur.ev[j];
+                top[j] = s[j >> 1][8 * (j & 1)];
 #pragma unroll
-            for (int q = 1; q < 8; ++q) top[j] = fmaxf(top[j], s[j >> 1][8 * (j & 1) + q]);
-            top[j] *= f[j];
+                for (int q = 1; q < 8; ++q) top[j] = fmaxf(top[j], s[j >> 1][8 * (j & 1) + q]);
+                top[j] *= f[j];
+            }
+            // the maximum moves only where it has grown by 2^8: until then p exceeds 1 and nothing is lost
+            m_top = fmaxf(m, max_halves(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))));
+            moves = __any(m_top > m + 8.0f);
+            m_new = moves ? m_top : m;
+            if constexpr (IO != kIoF32) {
+                const float big = fmaxf(fmaxf(top[0] + (float)ev[0], top[1] + (float)ev[1]), fmaxf(top[2] + (float)ev[2], top[3] + (float)ev[3]));
+                pexp_new = (int)fminf(fmaxf(__builtin_ceilf(max_halves(big) - m_new), -90.0f), 121.0f);
+            }
+        };
+        auto four = [&](int n) {  // p of registers 4*(n%4).. of s[n/4]: four keys of sixteen n/2
+            const int j = n >> 1;
+            float p[4];
+            if constexpr (IO != kIoF32) {
+                const float add = (float)(ev[j] - pexp_new + 8) - m_new;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n >> 2][4 * (n & 3) + q], f[j], add));
+                ladd += __builtin_ldexpf((p[0] + p[1]) + (p[2] + p[3]), pexp_new - 8 - ev[j]);
+                uint32_t w[N];
+                split4<N>(p[0], p[1], p[2], p[3], w);
+#pragma unroll
+                for (int t = 0; t < N; ++t) pn[t][n >> 2][n & 3] = w[t];
+            } else {
+                const float vs = pow2(ev[j]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n >> 2][4 * (n & 3) + q], f[j], -m_new));
+                    ladd += p[q];
+                    p[q] *= vs;
+                }
+#pragma unroll
+                for (int t = 0; t < N; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t w = pack16x2<kIoBF16>(p[2 * e], p[2 * e + 1]);
+                        float lo, hi;
+                        unpack16x2<kIoBF16>(w, lo, hi);
+                        p[2 * e] -= lo;
+                        p[2 * e + 1] -= hi;
+                        pn[t][j][2 * (n & 1) + e] = w;
+                    }
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+            if (i + 2 < NO) {
+                vx[(i + 2) % 3][0] = value_piece(vprev, i + 2, 0);
+                vx[(i + 2) % 3][1] = value_piece(vprev, i + 2, 1);
+            }
+            value_product(i, vx[i % 3][0], vx[i % 3][1]);
+            if (i == 0) begin();
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+                if (i > 0 && n * (NO - 1) / 8 == i - 1) four(n);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        float hi = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        const float m_new = fmaxf(m, max_halves(hi));
-        // the sums follow the maximum only where it has grown by 2^8: until then p exceeds 1 and nothing is lost
-        if (__any(m_new > m + 8.0f)) {
+        // (P is finished here and not beyond the branch below, where nothing runs beside it)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < PW; ++e) asm volatile("" : "+v"(pn[n][e]));
+        asm volatile("" : "+v"(ladd));
+        __builtin_amdgcn_sched_barrier(0);
+        if (moves) {
             const float c = __builtin_amdgcn_exp2f(m - m_new);
             l *= c;
 #pragma unroll
@@ -833,99 +958,42 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
             }
             m = m_new;
         }
-        if constexpr (IO != kIoF32) {
-            float big = fmaxf(fmaxf(top[0] + (float)ev[0], top[1] + (float)ev[1]), fmaxf(top[2] + (float)ev[2], top[3] + (float)ev[3]));
-            const int pexp = (int)fminf(fmaxf(__builtin_ceilf(max_halves(big) - m), -90.0f), 121.0f);
-            uint32_t pf[N][8];
+        l += ladd;
+        pexp = pexp_new;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float add = (float)(ev[j] - pexp + 8) - m;
-                float p[8], sum = 0.0f;
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j >> 1][8 * (j & 1) + q], f[j], add));
-                    sum += p[q];
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint32_t w[N];
-                    split4<N>(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3], w);
-#pragma unroll
-                    for (int n = 0; n < N; ++n) pf[n][2 * j + e] = w[n];
-                }
-                l += __builtin_ldexpf(sum, pexp - 8 - ev[j]);
-            }
-#pragma unroll
-            for (int i = 0; i < NO; ++i) {
-                const int d = 32 * i + col;
-                const i32x8 vf = join8(*reinterpret_cast<const u32x4 *>(&t.v[vword<D>(d, 2 * half)]),
-                                       *reinterpret_cast<const u32x4 *>(&t.v[vword<D>(d, 2 * half + 1)]));
-#pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const i32x8 pb = {(int)pf[n][0], (int)pf[n][1], (int)pf[n][2], (int)pf[n][3],
-                                      (int)pf[n][4], (int)pf[n][5], (int)pf[n][6], (int)pf[n][7]};
-                    o[i] = mfma8(vf, pb, o[i], 127, 119 + pexp - 4 * n);
-                }
-            }
-        } else {
-            u32x4 pf[N][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float vs = pow2(ev[j]);
-                float p[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j >> 1][8 * (j & 1) + q], f[j], -m));
-                    l += p[q];
-                    p[q] *= vs;
-                }
-#pragma unroll
-                for (int n = 0; n < N; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t w = pack16x2<kIoBF16>(p[2 * e], p[2 * e + 1]);
-                        float lo, hi2;
-                        unpack16x2<kIoBF16>(w, lo, hi2);
-                        p[2 * e] -= lo;
-                        p[2 * e + 1] -= hi2;
-                        pf[n][j][e] = w;
-                    }
-            }
-#pragma unroll
-            for (int i = 0; i < NO; ++i) {
-                const int d = 32 * i + col;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const u32x4 x = *reinterpret_cast<const u32x4 *>(&t.v[vword<D>(d, 2 * half + h)]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint2 lo = decode4<IO>(x[2 * e]), hi2 = decode4<IO>(x[2 * e + 1]);
-#pragma unroll
-                        for (int n = 0; n < N; ++n) o[i] = mfma16<IO>(u32x4{lo.x, lo.y, hi2.x, hi2.y}, pf[n][2 * h + e], o[i]);
-                    }
-                }
-            }
-        }
+            for (int e = 0; e < PW; ++e) pf[n][e] = pn[n][e];
 #pragma unroll
         for (int i = 0; i < NO; ++i) keep_in_acc(o[i]);
-        if (t.nan == it + 1) {  // rare: the dims in which this lane's row sees a NaN, half of them a lane
+        if (nan_here) {  // rare: the dims in which this lane's row sees a NaN, half of them a lane
             const int32_t seen = lim - t0;
 #pragma unroll 1
             for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d) {
                 uint32_t bad_d = 0;
 #pragma unroll 1
-                for (int w = 0; w < 16; ++w) bad_d |= t.nanv[w][d] & ((1u << min(max(seen - 4 * w, 0), 4)) - 1);
-                if (bad_d) bad[r][d >> 5] |= 1u << (d & 31);
+                for (int w = 0; w < 16; ++w) bad_d |= lds.nanv[it & 1][w][d] & ((1u << min(max(seen - 4 * w, 0), 4)) - 1);
+                if (bad_d) lds.bad[r][d >> 5] |= 1u << (d & 31);
             }
         }
     }
-    for (; it < n_tiles; ++it, next = then) stage();
+    // (its buffer is written again two barriers from here)
+#pragma unroll
+    for (int i = 0; i < NO; ++i) value_product(i, value_piece(vprev, i, 0), value_piece(vprev, i, 1));
+    for (; it < n_tiles; ++it, turn()) {
+        __syncthreads();
+        clean_v(it + 1, next);
+        turn_pages(it + 2);
+#pragma unroll
+        for (int n = 0; n < kSlices; ++n) store_slice(n, it + 1, vnext);
+        then = load_tile(it + 2);
+    }
 
     l += __shfl_xor(l, 32);
     if (!live) return;
 #pragma unroll
     for (int i = 0; i < NO; ++i) {
-        const uint32_t b = bad[r][i] >> (4 * half);  // both halves of a row's dims are marked by lanes of this wave
+        const uint32_t b = lds.bad[r][i] >> (4 * half);  // both halves of a row's dims are marked by lanes of this wave
         if (b)
 #pragma unroll
             for (int q = 0; q < 16; ++q)
