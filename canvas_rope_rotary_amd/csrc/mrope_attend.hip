@@ -461,8 +461,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
 //
 // S^T = K Q^T runs in 16 bits (32 x 32 x 16): the codes of K are exact in bf16 and fp16, so the queries'
 // own type is exact too and fp32 queries take three bf16 terms (each the nearest to what the terms before
-// it leave).  K lies in LDS as it does in the cache and is decoded behind the matrix unit's back; its page
-// scale joins the softmax's factor.  (The 8-bit instruction would take K undecoded, but sums a product's
+// it leave).  K is decoded once, on its way to LDS; its page scale joins the softmax's factor.  (The 8-bit instruction would take K undecoded, but sums a product's
 // 64 terms with some 13 bits below the largest: measured, the scores' sums then were off by 1e-6 of
 // themselves where 32 bits give 4e-8.)
 //
@@ -518,21 +517,26 @@ __device__ __forceinline__ u32x4 decode8(uint32_t u, uint32_t v)
         return u32x4{bf16_pair<false>(u, 1.0f), bf16_pair<true>(u, 1.0f), bf16_pair<false>(v, 1.0f), bf16_pair<true>(v, 1.0f)};
 }
 
-// Four values to N terms of four codes each.
+// Four values to N terms of four codes each; all but the first are coded 2^4 finer than the one before.
 template <int N>
 __device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&t)[N])
 {
+    typedef short i16x2 __attribute__((ext_vector_type(2)));
+    t[0] = pack_e4m3(a, b, c, d);
+    float finer = 1.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        t[i] = pack_e4m3(a, b, c, d);
-        if (i + 1 < N) {
-            const kv8_f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)t[i], false);
-            const kv8_f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)t[i], true);
-            a = (a - lo[0]) * 16.0f;
-            b = (b - lo[1]) * 16.0f;
-            c = (c - hi[0]) * 16.0f;
-            d = (d - hi[1]) * 16.0f;
-        }
+    for (int i = 1; i < N; ++i) {
+        const kv8_f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)t[i - 1], false);
+        const kv8_f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)t[i - 1], true);
+        a -= lo[0] * finer;
+        b -= lo[1] * finer;
+        c -= hi[0] * finer;
+        d -= hi[1] * finer;
+        finer *= 0.0625f;  // the conversion divides by it
+        i16x2 w = {0, 0};
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, finer, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, finer, true);
+        t[i] = __builtin_bit_cast(uint32_t, w);
     }
 }
 
@@ -541,18 +545,13 @@ constexpr int kVB = D / 16;  // dims of V a thread transposes, for four keys
 
 template <int D>
 struct alignas(16) ManyLds {
-    uint8_t k[2][64][D + 16];           // keys, as they lie in the cache
+    uint8_t k[2][64][2 * D + 16];       // 16-bit keys
     uint32_t v[3][16 * (D + 16)];       // word of (dim d, keys 4w..): see vword()
     uint8_t nanv[2][16][D];             // bit b of [w][d]: key 4w + b has a NaN in dim d (written where a row may not see it)
     uint32_t bad[kManyRows][D / 32];    // bit d of a row: it saw a NaN in that dim of V
     int32_t nan[2];                     // 1 + the last tile in which `nanv` has a bit
-};
-
-// What a tile's sixteens of keys share: their scales and whether they have a page.
-struct Sixteens {
-    float ks[4];    // K's scale
-    int32_t ev[4];  // exponent of V's scale
-    uint32_t live;  // bit j
+    float ks[2][4], ev[2][4];           // by 16 keys: K's scale, the exponent of V's
+    int32_t dead[2][4];                 // nonzero: no page
 };
 
 template <int D>
@@ -561,11 +560,19 @@ __device__ __forceinline__ int vword(int d, int piece)
     return 16 * d + 16 * (d / kVB<D>) + 4 * (piece ^ ((d >> 1) & 3));
 }
 
+// The largest of three (of the others where one is NaN), without the canonicalisation that fmaxf costs.
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    return r;
+}
+
 // The larger of a lane's and its counterpart's in the other half of the wave.
 __device__ __forceinline__ float max_halves(float x)
 {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    return max3(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[1]));
 }
 
 __device__ __forceinline__ i32x8 join8(u32x4 x, u32x4 y)
@@ -613,14 +620,14 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     const float factor = a.scale_log2 != 0.0f ? __builtin_fabsf(a.scale_log2) : 1.0f;
     const float sign = a.scale_log2 < 0.0f ? -1.0f : (a.scale_log2 > 0.0f ? 1.0f : 0.0f);
 
-    // Q of the lane's row: step s takes dims 32*(s/2) + 16*half + 8*(s%2) .. + 7, as a 16-byte piece of K holds them
+    // Q: dims 16*s + 8*half .. + 7 of the lane's row
     u32x4 qf[QT][NS];
     {
-        const int64_t off = (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head + half * 16;
+        const int64_t off = (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head + half * 8;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             float x[8];
-            unpack8<IO>(load8<IO>(a.q, off + 32 * (s >> 1) + 8 * (s & 1)), x);
+            unpack8<IO>(load8<IO>(a.q, off + s * 16), x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] *= sign;
 #pragma unroll
@@ -653,9 +660,9 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
 
     // Pages and scales of 16 tiles, a sixteen of keys a lane; those of the next 16 are fetched on the way.
     struct Lanes {
-        int32_t page;  // -1 = none
-        float ks;
-        int32_t ev;
+        int64_t at;   // bytes to the page (a key without one, or past the last tile, reads page 0)
+        float ks, ev;
+        int32_t dead;
     };
     auto fetch_pages = [&](int group) {
         const int32_t tok = c0 + (group * 64 + lane) * 16;
@@ -664,45 +671,56 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
         return page >= 0 && page < kv.num_blocks ? page : -1;
     };
     auto fetch_scales = [&](int32_t page) {
-        Lanes x{page, 1.0f, 0};
+        Lanes x{0, 1.0f, 0.0f, 1};
         if (page >= 0) {
+            x.at = page * kv.c_block;
             x.ks = kv.k_scale[(int64_t)page * kv.nk + kvh];
-            x.ev = scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]);
+            x.ev = (float)scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]);
+            x.dead = 0;
         }
         return x;
     };
-    Lanes here{-1, 1.0f, 0}, ahead{-1, 1.0f, 0};
+    Lanes here{0, 1.0f, 0.0f, 1};
+    int32_t page_ahead = -1;
     auto turn_pages = [&](int i) {  // before load_tile(i), in order
-        const int at = i & 15;
-        if (at == 0) here = i ? ahead : fetch_scales(fetch_pages(0));
-        if (at == 4) ahead.page = fetch_pages((i >> 4) + 1);
-        if (at == 8) ahead = fetch_scales(ahead.page);
+        if (i & 7) return;
+        if (i & 8) page_ahead = fetch_pages((i >> 4) + 1);
+        else here = fetch_scales(i ? page_ahead : fetch_pages(0));
     };
+    auto page_at = [&](int l) {
+        const uint32_t lo = __shfl((int)(uint32_t)here.at, l), hi = __shfl((int)(uint32_t)((uint64_t)here.at >> 32), l);
+        return (int64_t)(((uint64_t)hi << 32) | lo);
+    };
+    float ks_lane = 1.0f, ev_lane = 0.0f;  // of the tile loaded last, where this lane holds one of its sixteens
+    int32_t dead_lane = 1, info = -1;
     auto load_tile = [&](int i) {
         const int at = (i & 15) * 4;
-        Sixteens x;
-        x.live = 0;
+        const uint8_t *pk[KP];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x.ks[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(here.ks), at + j));
-            x.ev[j] = __builtin_amdgcn_readlane(here.ev, at + j);
-            x.live |= __builtin_amdgcn_readlane(here.page, at + j) >= 0 ? 1u << j : 0u;
-        }
-        // (a key without a page, or of a tile past the last, reads page 0)
+        for (int p = 0; p < KP; ++p) pk[p] = kv.k + page_at(at + ((kr + p * KR) >> 4)) + koff[p];
+        const uint8_t *pv = kv.v + page_at(at + (vt >> 2)) + voff;
 #pragma unroll
-        for (int p = 0; p < KP; ++p)
-            kreg[p] = *reinterpret_cast<const u32x4 *>(kv.k + max(__shfl(here.page, at + ((kr + p * KR) >> 4)), 0) * kv.c_block + koff[p]);
-        const uint8_t *pv = kv.v + max(__shfl(here.page, at + (vt >> 2)), 0) * kv.c_block + voff;
+        for (int p = 0; p < KP; ++p) kreg[p] = *reinterpret_cast<const u32x4 *>(pk[p]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) vreg[j] = load_vrow<D>(pv + j * kv.c_tok);
-        return x;
+        info = lane - at;
+        ks_lane = here.ks;
+        ev_lane = here.ev;
+        dead_lane = here.dead;
+    };
+    auto store_info = [&](int i) {
+        if ((unsigned)info < 4u) {  // every wave writes the same
+            lds.ks[i & 1][info] = ks_lane;
+            lds.ev[i & 1][info] = ev_lane;
+            lds.dead[i & 1][info] = dead_lane;
+        }
     };
     // What no row sees may hold anything: it must not reach the product; and where some rows see a NaN and
     // others do not, the product goes on without it and the rows are told.
-    auto clean_v = [&](int i, const Sixteens &x) {
+    auto clean_v = [&](int i) {
         const int32_t t0 = c0 + i * 64;
-        if (t0 + 64 <= first && x.live == 15u) return;
-        const bool has = (x.live >> (vt >> 2)) & 1;
+        if (t0 + 64 <= first && !__any((unsigned)info < 4u && dead_lane)) return;
+        const bool has = !__shfl(here.dead, (i & 15) * 4 + (vt >> 2));
         bool nan = false;
 #pragma unroll
         for (int w = 0; w < VB / 4; ++w) {
@@ -728,7 +746,10 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     constexpr int kSlices = KP + VB / 4;
     auto store_slice = [&](int n, int i, uint32_t *vbuf) {
         if (n < KP) {
-            *reinterpret_cast<u32x4 *>(&lds.k[i & 1][kr][kc] + n * KR * (D + 16)) = kreg[n < KP ? n : 0];
+            uint8_t *kb = &lds.k[i & 1][kr][2 * kc] + n * KR * (2 * D + 16);
+            const u32x4 x = kreg[n < KP ? n : 0];
+            *reinterpret_cast<u32x4 *>(kb) = decode8<IO>(x[0], x[1]);
+            *reinterpret_cast<u32x4 *>(kb + 16) = decode8<IO>(x[2], x[3]);
             return;
         }
         const int w = n - KP;
@@ -783,15 +804,14 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     for (int i = tid; i < kManyRows * NO; i += 64 * kManyWaves) lds.bad[i / NO][i % NO] = 0;
     for (int i = tid; i < 16 * (D + 16); i += 64 * kManyWaves) lds.v[2][i] = 0;  // before the first tile: nothing
     __syncthreads();
-    Sixteens cur{}, next{}, then{};
     if (n_tiles > 0) {
         turn_pages(0);
-        cur = load_tile(0);
-        clean_v(0, cur);
+        load_tile(0);
+        clean_v(0);
+        store_info(0);
 #pragma unroll
         for (int n = 0; n < kSlices; ++n) store_slice(n, 0, lds.v[0]);
-        turn_pages(1);
-        next = load_tile(1);
+        load_tile(1);
     }
     // V's buffers of tiles it - 1, it and it + 1
     uint32_t *vprev = lds.v[2], *vcur = lds.v[0], *vnext = lds.v[1];
@@ -800,8 +820,6 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
         vprev = vcur;
         vcur = vnext;
         vnext = x;
-        cur = next;
-        next = then;
     };
     // tiles that this wave's rows see, then those that it only helps to stage
     const int n_mine = min(n_tiles, wlim > c0 ? (wlim - c0 + 63) / 64 : 0);
@@ -809,48 +827,51 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     for (; it < n_mine; ++it, turn()) {
         const int32_t t0 = c0 + it * 64;
         __syncthreads();  // tile `it` is in LDS, and tiles it - 1 (K) and it - 2 (V) have been read
-        clean_v(it + 1, next);
+        clean_v(it + 1);
+        store_info(it + 1);
         turn_pages(it + 2);
         __builtin_amdgcn_sched_barrier(0);
 
-        // The scores, step by step: a 16-byte piece of keys is two steps of the product.  Pieces are read
-        // kAhead steps before their use and decoded one before, while the matrix unit is busy; beside
-        // them the next tile goes to LDS, and the one after it is asked for.  (Past the last tile both are done for nobody.)
-        constexpr int NJ = NS, kAhead = NJ < 6 ? 2 : 6;
+        // The scores, step by step, their operands read kAhead steps before their use; beside them the
+        // next tile goes to LDS, and the one after it is asked for.  (Past the last tile both are done for nobody.)
+        constexpr int kAhead = NS < 8 ? 2 : 4;
         const uint8_t *kb = &lds.k[it & 1][col][16 * half];
-        auto key_piece = [&](int j) { return *reinterpret_cast<const u32x4 *>(kb + (j & 1) * 32 * (D + 16) + (j >> 1) * 32); };
+        auto key_piece = [&](int k, int h) { return *reinterpret_cast<const u32x4 *>(kb + h * 32 * (2 * D + 16) + k * 32); };
         f32x16 s[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int q = 0; q < 16; ++q) s[h][q] = 0.0f;
-        u32x4 piece[kAhead], ka[2], kn[2];
+        u32x4 piece[kAhead][2];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) piece[j] = key_piece(j);
-        ka[0] = decode8<IO>(piece[0][0], piece[0][1]);
-        ka[1] = decode8<IO>(piece[0][2], piece[0][3]);
+        for (int k = 0; k < kAhead; ++k) {
+            piece[k][0] = key_piece(k, 0);
+            piece[k][1] = key_piece(k, 1);
+        }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            if (j + kAhead < NJ) piece[j % kAhead] = key_piece(j + kAhead);
+        for (int k = 0; k < NS; ++k) {
+            constexpr int kPer = (kSlices + NS / 2 - 1) / (NS / 2);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int n = 0; n < QT; ++n) s[j & 1] = mfma16<IO>(ka[u], qf[n][(j & ~1) + u], s[j & 1]);
-            constexpr int kPer = (kSlices + NJ / 2 - 1) / (NJ / 2);
-#pragma unroll
-            for (int n = j * kPer; n < (j + 1) * kPer; ++n)
-                if (n < kSlices) store_slice(n, it + 1, vnext);
-            if (j == NJ / 2) then = load_tile(it + 2);
-            if (j + 1 < NJ) {
-                const u32x4 x = piece[(j + 1) % kAhead];
-                kn[0] = decode8<IO>(x[0], x[1]);
-                kn[1] = decode8<IO>(x[2], x[3]);
-                ka[0] = kn[0];
-                ka[1] = kn[1];
+                for (int n = 0; n < QT; ++n) s[h] = mfma16<IO>(piece[k % kAhead][h], qf[n][k], s[h]);
+                if (k + kAhead < NS) piece[k % kAhead][h] = key_piece(k + kAhead, h);
             }
+#pragma unroll
+            for (int n = k * kPer; n < (k + 1) * kPer; ++n)
+                if (n < kSlices) store_slice(n, it + 1, vnext);
+            if (k == NS / 2) load_tile(it + 2);
             __builtin_amdgcn_sched_barrier(0);
         }
         const bool nan_here = lds.nan[it & 1] == it + 1;
+        float f[4], ev[4];  // by 16 keys: the scores' factor, the exponent of V's scale
+        int32_t dead[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[j] = lds.ks[it & 1][j];
+            ev[j] = lds.ev[it & 1][j];
+            dead[j] = lds.dead[it & 1][j];
+        }
         u32x4 vx[3][2];  // V's operands, two products ahead
 #pragma unroll
         for (int i = 0; i < 2 && i < NO; ++i) {
@@ -859,55 +880,54 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
         }
 
         // register 4a + b of s[h]: key 32h + 8a + 4*half + b
-        if (t0 + 64 > wfirst || cur.live != 15u) {
+        if (t0 + 64 > wfirst || __any(dead[0] | dead[1] | dead[2] | dead[3])) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int key = 32 * h + 8 * (q >> 2) + 4 * half + (q & 3);
-                    if (t0 + key >= lim || !((cur.live >> (2 * h + (q >> 3))) & 1)) s[h][q] = -__builtin_inff();
+                    if (t0 + key >= lim || dead[2 * h + (q >> 3)]) s[h][q] = -__builtin_inff();
                 }
         }
         __builtin_amdgcn_sched_barrier(0);
         // The softmax, and between its steps the tile before's product with V.
-        float f[4], top[4];  // by 16 keys: the scores' factor, the largest score
-        int ev[4], pexp_new = 0;
-        float m_new = m, m_top = m, ladd = 0.0f;
+        float top[4], m_new = m, ladd = 0.0f;
+        int pexp_new = 0;
         bool moves = false;
         u32x4 pn[N][PW];
         auto begin = [&]() {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[j] = factor * cur.ks[j];
-                ev[j] = cur.ev[j];
-                top[j] = s[j >> 1][8 * (j & 1)];
-#pragma unroll
-                for (int q = 1; q < 8; ++q) top[j] = fmaxf(top[j], s[j >> 1][8 * (j & 1) + q]);
-                top[j] *= f[j];
+            for (int j = 0; j < 4; ++j) {  // the largest score of each sixteen
+                const int h = j >> 1, q = 8 * (j & 1);
+                f[j] *= factor;
+                top[j] = max3(max3(max3(s[h][q], s[h][q + 1], s[h][q + 2]), s[h][q + 3], s[h][q + 4]), s[h][q + 5], s[h][q + 6]);
+                top[j] = max3(top[j], s[h][q + 7], s[h][q + 7]) * f[j];
             }
             // the maximum moves only where it has grown by 2^8: until then p exceeds 1 and nothing is lost
-            m_top = fmaxf(m, max_halves(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))));
+            const float m_top = max_halves(max3(max3(top[0], top[1], top[2]), top[3], m));
             moves = __any(m_top > m + 8.0f);
             m_new = moves ? m_top : m;
             if constexpr (IO != kIoF32) {
-                const float big = fmaxf(fmaxf(top[0] + (float)ev[0], top[1] + (float)ev[1]), fmaxf(top[2] + (float)ev[2], top[3] + (float)ev[3]));
+                const float big = max3(max3(top[0] + ev[0], top[1] + ev[1], top[2] + ev[2]), top[3] + ev[3], -1e30f);
                 pexp_new = (int)fminf(fmaxf(__builtin_ceilf(max_halves(big) - m_new), -90.0f), 121.0f);
             }
         };
+        float sum4[8];
         auto four = [&](int n) {  // p of registers 4*(n%4).. of s[n/4]: four keys of sixteen n/2
             const int j = n >> 1;
             float p[4];
             if constexpr (IO != kIoF32) {
-                const float add = (float)(ev[j] - pexp_new + 8) - m_new;
+                const float up = ev[j] - (float)(pexp_new - 8), add = up - m_new;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n >> 2][4 * (n & 3) + q], f[j], add));
-                ladd += __builtin_ldexpf((p[0] + p[1]) + (p[2] + p[3]), pexp_new - 8 - ev[j]);
+                sum4[n] = (p[0] + p[1]) + (p[2] + p[3]);
+                if (n & 1) ladd += __builtin_ldexpf(sum4[n - 1] + sum4[n], -(int)up);
                 uint32_t w[N];
                 split4<N>(p[0], p[1], p[2], p[3], w);
 #pragma unroll
                 for (int t = 0; t < N; ++t) pn[t][n >> 2][n & 3] = w[t];
             } else {
-                const float vs = pow2(ev[j]);
+                const float vs = pow2((int)ev[j]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n >> 2][4 * (n & 3) + q], f[j], -m_new));
@@ -982,11 +1002,12 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     for (int i = 0; i < NO; ++i) value_product(i, value_piece(vprev, i, 0), value_piece(vprev, i, 1));
     for (; it < n_tiles; ++it, turn()) {
         __syncthreads();
-        clean_v(it + 1, next);
+        clean_v(it + 1);
+        store_info(it + 1);
         turn_pages(it + 2);
 #pragma unroll
         for (int n = 0; n < kSlices; ++n) store_slice(n, it + 1, vnext);
-        then = load_tile(it + 2);
+        load_tile(it + 2);
     }
 
     l += __shfl_xor(l, 32);
