@@ -549,6 +549,7 @@ struct alignas(16) ManyLds {
     uint32_t v[3][16 * (D + 16)];       // word of (dim d, keys 4w..): see vword()
     uint8_t nanv[2][16][D];             // bit b of [w][d]: key 4w + b has a NaN in dim d (written where a row may not see it)
     uint32_t bad[kManyRows][D / 32];    // bit d of a row: it saw a NaN in that dim of V
+    int32_t any_bad;
     int32_t nan[2];                     // 1 + the last tile in which `nanv` has a bit
     float ks[2][4], ev[2][4];           // by 16 keys: K's scale, the exponent of V's
     int32_t dead[2][4];                 // nonzero: no page
@@ -801,6 +802,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     };
 
     if (tid < 2) lds.nan[tid] = 0;
+    if (tid == 2) lds.any_bad = 0;
     for (int i = tid; i < kManyRows * NO; i += 64 * kManyWaves) lds.bad[i / NO][i % NO] = 0;
     for (int i = tid; i < 16 * (D + 16); i += 64 * kManyWaves) lds.v[2][i] = 0;  // before the first tile: nothing
     __syncthreads();
@@ -993,7 +995,10 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
                 uint32_t bad_d = 0;
 #pragma unroll 1
                 for (int w = 0; w < 16; ++w) bad_d |= lds.nanv[it & 1][w][d] & ((1u << min(max(seen - 4 * w, 0), 4)) - 1);
-                if (bad_d) lds.bad[r][d >> 5] |= 1u << (d & 31);
+                if (bad_d) {
+                    lds.bad[r][d >> 5] |= 1u << (d & 31);
+                    lds.any_bad = 1;
+                }
             }
         }
     }
@@ -1012,25 +1017,26 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
 
     l += __shfl_xor(l, 32);
     if (!live) return;
+    if (lds.any_bad) {
 #pragma unroll
-    for (int i = 0; i < NO; ++i) {
-        const uint32_t b = lds.bad[r][i] >> (4 * half);  // both halves of a row's dims are marked by lanes of this wave
-        if (b)
+        for (int i = 0; i < NO; ++i) {
+            const uint32_t b = lds.bad[r][i] >> (4 * half);  // both halves of a row's dims are marked by lanes of this wave
 #pragma unroll
             for (int q = 0; q < 16; ++q)
                 if ((b >> (8 * (q >> 2) + (q & 3))) & 1) o[i][q] = __builtin_nanf("");
+        }
     }
     const int64_t tok = tl.t0 + row / g;
     const int head = kvh * g + row % g;
     if (lim_last <= chunk) {
-        const float inv = 1.0f / l;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (a row that saw nothing has summed nothing)
 #pragma unroll
         for (int i = 0; i < NO; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float y[4];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) y[b] = l == 0.0f ? 0.0f : o[i][4 * e + b] * inv;
+                for (int b = 0; b < 4; ++b) y[b] = o[i][4 * e + b] * inv;
                 const int64_t at = tok * a.o_tok + head * a.o_head + 32 * i + 8 * e + 4 * half;
                 if constexpr (IO == kIoF32)
                     *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
