@@ -117,7 +117,7 @@ def load():
     lib.mrope_pages_workspace_bytes.argtypes = [I64, I64]
     lib.mrope_pages_workspace_bytes.restype = U64
     state = [P, I64, *tables, P, I64]  # refcount, num_blocks, tables, seq_lens, n_rows
-    pools = [ctypes.POINTER(MropePool), I32]
+    pools = [P, I32]  # mrope_pool[], n_pools
     lib.mrope_pages_grow.argtypes = [*state, I32, P, P, I32, P, P, U64, P]
     lib.mrope_pages_free.argtypes = [*state, P, I32, P]
     lib.mrope_pages_fork.argtypes = [*state, I32, P, P, I32, P, *pools, P, U64, P]
