@@ -31,41 +31,50 @@ struct Tile {
     int64_t seen;       // positions the sequence's tables can hold and its context has
 };
 
+// Tile k of R rows of sequence s, whose first token is t0 of len.
+template <int R>
+__device__ __forceinline__ bool make_tile(const Attend &a, int g, int32_t s, int32_t t0, int32_t len, int64_t k, Tile &t)
+{
+    t.s = s;
+    t.t0 = t0;
+    t.rows = len * g;
+    if (k * R >= t.rows) return false;
+    t.row0 = (int32_t)k * R;
+    const int64_t ctx = max(a.ctx[s], 0);
+    t.past = ctx - len;
+    t.seen = min(ctx, (int64_t)a.kv.table_width << a.kv.bs_shift);
+    return true;
+}
+
+template <int R>
+__device__ __forceinline__ bool make_tile(const Attend &a, int g, int32_t s, int64_t k, Tile &t)
+{
+    if (!a.cu) return make_tile<R>(a, g, s, s, 1, k, t);
+    const int32_t t0 = a.cu[s];
+    return make_tile<R>(a, g, s, t0, (int32_t)min((int64_t)a.cu[s + 1], a.n_tokens) - t0, k, t);
+}
+
 // Tile w of R rows.  Sequence s begins at tile floor(cu[s] * g / R) + s: the key grows by at least
 // ceil(rows / R) a sequence.
 template <int R>
 __device__ __forceinline__ bool find_tile(const Attend &a, int g, int64_t w, int lane, Tile &t)
 {
-    int64_t first;
-    int32_t len = 1;
-    if (a.cu) {
-        int32_t lo = 0, hi = a.n_seqs;
-        while (hi - lo > 1) {
-            const int32_t step = (hi - lo + 63) / 64;
-            const int32_t p = lo + lane * step;
-            const bool le = p < hi && (int64_t)a.cu[min(p, a.n_seqs)] * g / R + p <= w;
-            const int c = __builtin_popcountll(__ballot(le));
-            hi = min(hi, lo + c * step);
-            lo += (c - 1) * step;
-        }
-        t.s = __builtin_amdgcn_readfirstlane(lo);
-        t.t0 = a.cu[t.s];
-        len = (int32_t)min((int64_t)a.cu[t.s + 1], a.n_tokens) - t.t0;
-        first = (int64_t)t.t0 * g / R + t.s;
-    } else {
+    if (!a.cu) {
         const int32_t per = (g + R - 1) / R;
-        t.s = (int32_t)(w / per);
-        t.t0 = t.s;
-        first = (int64_t)t.s * per;
+        const int32_t s = (int32_t)(w / per);
+        return make_tile<R>(a, g, s, w - (int64_t)s * per, t);
     }
-    t.rows = len * g;
-    const int64_t row0 = (w - first) * R;
-    if (row0 >= t.rows) return false;
-    t.row0 = (int32_t)row0;
-    const int64_t ctx = max(a.ctx[t.s], 0);
-    t.past = ctx - len;
-    t.seen = min(ctx, (int64_t)a.kv.table_width << a.kv.bs_shift);
-    return true;
+    int32_t lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {
+        const int32_t step = (hi - lo + 63) / 64;
+        const int32_t p = lo + lane * step;
+        const bool le = p < hi && (int64_t)a.cu[min(p, a.n_seqs)] * g / R + p <= w;
+        const int c = __builtin_popcountll(__ballot(le));
+        hi = min(hi, lo + c * step);
+        lo += (c - 1) * step;
+    }
+    const int32_t s = __builtin_amdgcn_readfirstlane(lo);
+    return make_tile<R>(a, g, s, w - ((int64_t)a.cu[s] * g / R + s), t);
 }
 
 // Positions that the row sees: [0, row_limit), 0 for none (at most 2^27: a table holds no more).
@@ -102,8 +111,8 @@ __device__ __forceinline__ int32_t chunk_of(int32_t lim, int n_chunks, int unit)
 template <int NT>
 constexpr int kRowsOf = NT == 2 ? 8 : 4;
 constexpr int kFewWaves = 4;
-constexpr int kFewUnit = 128;    // a block of 32 tokens a wave
-constexpr int kFewMost = 4096;   // tokens of a chunk: a lane keeps the page of one 16-token half block
+constexpr int kFewUnit = 128;     // a block of 32 tokens a wave
+constexpr int kFewPages = 4096;   // tokens whose pages a wave looks up at once: a 16-token half block a lane
 
 __device__ __forceinline__ float row_ror8(float x)
 {
@@ -173,14 +182,139 @@ struct Partial {  // of a tile and chunk, in the workspace
     float o[R][D];
 };
 
+// The work is cut by the batch's contexts: chunks of all sequences are about as long as one another, in
+// as many as run at once (`budget` for a KV head), so a long context among short ones does not finish
+// last.  Sequence s has tiles_s tiles; a tile is cut into n_s chunks, n_s - 1 < seen_s / unit for a unit that
+// makes sum_s tiles_s seen_s / unit <= budget.  So there are at most tiles + budget chunks, at most
+// `budget` tiles are cut, and those have at most 2 * budget chunks, which get a slot of the workspace each.
+struct Cut {
+    int32_t s, tile;  // sequence, tile of it
+    int32_t slot, n;  // of the tile's first chunk, chunks
+};
+struct alignas(16) CutList {  // at the workspace's start, for the join
+    int32_t n;
+    Cut cut[1];
+};
+constexpr size_t cut_list_bytes(int64_t n) { return 16 + (size_t)n * sizeof(Cut); }
+
+struct FewPlan {
+    int32_t budget;            // chunks of a KV head that run at once
+    int32_t max_cut, max_slots;  // tiles that may be cut, and chunks of them (none: nothing to join)
+};
+
+template <int R>
+__device__ __forceinline__ int32_t tiles_of(const Attend &a, int g, int32_t s, bool in)
+{
+    if (!in) return 0;
+    if (!a.cu) return (g + R - 1) / R;
+    const int64_t len = min((int64_t)a.cu[s + 1], a.n_tokens) - a.cu[s];
+    return (int32_t)((max(len, (int64_t)0) * g + R - 1) / R);
+}
+
+__device__ __forceinline__ int32_t seen_of(const Attend &a, int32_t s, bool in)
+{
+    return in ? (int32_t)min((int64_t)max(a.ctx[s], 0), (int64_t)a.kv.table_width << a.kv.bs_shift) : 0;
+}
+
+struct Sums {  // of a range of sequences: chunks, tiles that are cut, chunks of those
+    int32_t all, cut, slots;
+    __device__ void add(int32_t tiles, int32_t seen, int32_t unit)
+    {
+        const int32_t n = max((int32_t)(((int64_t)seen + unit - 1) / unit), 1);
+        all += tiles * n;
+        if (n > 1) cut += tiles, slots += tiles * n;
+    }
+    __device__ Sums scan(int lane) const  // the lanes' up to this one's
+    {
+        Sums r = *this;
+#pragma unroll
+        for (int x = 1; x < 64; x *= 2) {
+            const Sums o = {__shfl_up(r.all, x), __shfl_up(r.cut, x), __shfl_up(r.slots, x)};
+            if (lane >= x) r.all += o.all, r.cut += o.cut, r.slots += o.slots;
+        }
+        return r;
+    }
+};
+
+// Chunk w of the call: `z` of tile `c`, whose place in the list of cut tiles is `rank`.
+template <int R>
+__device__ __forceinline__ bool find_chunk(const Attend &a, int g, int64_t w, int32_t budget, int lane, Cut &c, int32_t &z,
+                                           int32_t &rank, int32_t &n_cut)
+{
+    const int32_t per = (a.n_seqs + 63) / 64;  // sequences of a lane
+    const int64_t s0 = (int64_t)lane * per;
+    int64_t total = 0;
+    int32_t tiles = 0, seen = 0;
+    for (int32_t i = 0; i < per; ++i) {
+        const bool in = s0 + i < a.n_seqs;
+        tiles = tiles_of<R>(a, g, (int32_t)(s0 + i), in);
+        seen = seen_of(a, (int32_t)(s0 + i), in);
+        total += (int64_t)tiles * seen;
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) total += __shfl_xor(total, x);
+    const int64_t want = (total + budget - 1) / budget;
+    const int32_t unit = (int32_t)max(min((want + kFewUnit - 1) / kFewUnit * kFewUnit, (int64_t)1 << 30), (int64_t)kFewUnit);
+
+    Sums own = {};
+    if (per == 1) {
+        own.add(tiles, seen, unit);
+    } else {
+        for (int32_t i = 0; i < per; ++i) {
+            const bool in = s0 + i < a.n_seqs;
+            own.add(tiles_of<R>(a, g, (int32_t)(s0 + i), in), seen_of(a, (int32_t)(s0 + i), in), unit);
+        }
+    }
+    Sums up = own.scan(lane);
+    n_cut = __builtin_amdgcn_readlane(up.cut, 63);
+    if (w >= __builtin_amdgcn_readlane(up.all, 63)) return false;
+    int at = __builtin_popcountll(__ballot(up.all <= w));  // the lane whose sequences hold it
+    Sums base = {__builtin_amdgcn_readlane(up.all - own.all, at), __builtin_amdgcn_readlane(up.cut - own.cut, at),
+                 __builtin_amdgcn_readlane(up.slots - own.slots, at)};
+    int32_t s = at;
+    if (per > 1) {
+        const int32_t first = at * per, last = min(first + per, a.n_seqs);
+        for (s = first;; s += 64) {  // (ends: the chunk is one of these)
+            const bool in = s + lane < last;
+            tiles = tiles_of<R>(a, g, s + lane, in);
+            seen = seen_of(a, s + lane, in);
+            own = {};
+            own.add(tiles, seen, unit);
+            up = own.scan(lane);
+            if (base.all + __builtin_amdgcn_readlane(up.all, 63) > w || s + 64 >= last) break;
+            base.all += __builtin_amdgcn_readlane(up.all, 63);
+            base.cut += __builtin_amdgcn_readlane(up.cut, 63);
+            base.slots += __builtin_amdgcn_readlane(up.slots, 63);
+        }
+        at = min(__builtin_popcountll(__ballot(base.all + up.all <= w)), 63);
+        base.all += __builtin_amdgcn_readlane(up.all - own.all, at);
+        base.cut += __builtin_amdgcn_readlane(up.cut - own.cut, at);
+        base.slots += __builtin_amdgcn_readlane(up.slots - own.slots, at);
+        s += at;
+    }
+    seen = __builtin_amdgcn_readlane(seen, at);
+    c.s = s;
+    c.n = max((int32_t)(((int64_t)seen + unit - 1) / unit), 1);
+    const int32_t k = (int32_t)w - base.all;
+    c.tile = k / c.n;
+    z = k - c.tile * c.n;
+    c.slot = base.slots + c.tile * c.n;
+    rank = base.cut + c.tile;
+    return true;
+}
+
 template <int IO>
 __device__ __forceinline__ void store_out8(const Attend &a, int64_t off, const float (&y)[8])
 {
     store8<IO>(a.out, off, pack8<IO>(y));
 }
 
+// Workgroups of a compute unit that the registers let run at once: the accumulators and the block on its
+// way grow with D.
+constexpr int few_resident(int head_dim) { return head_dim == 256 ? 2 : (head_dim == 128 ? 3 : 4); }
+
 template <int IO, int D, int NT>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a, int n_chunks)
+__global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_kernel(Attend a, FewPlan p)
 {
     constexpr int R = kRowsOf<NT>;
     constexpr int NK = D / 64;   // 16-byte pieces of a key a lane holds
@@ -188,24 +322,48 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
     const Kv8 &kv = a.kv;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 15, grp = lane >> 4;
-    const int g = a.nq / kv.nk, kvh = blockIdx.y, z = blockIdx.z;
+    const int g = a.nq / kv.nk, kvh = blockIdx.y;
 
+    Cut cut;
+    int32_t z, rank, n_cut;
+    CutList *list = static_cast<CutList *>(a.workspace);
+    const bool found = find_chunk<R>(a, g, blockIdx.x, p.budget, lane, cut, z, rank, n_cut);
+    if (p.max_cut > 0 && blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) list->n = min(n_cut, p.max_cut);
+    if (!found) return;
+    if (cut.n > 1) {
+        if (rank >= p.max_cut || cut.slot + cut.n > p.max_slots) return;  // (not for offsets that grow)
+        if (z == 0 && kvh == 0 && threadIdx.x == 0) list->cut[rank] = cut;
+    }
     Tile tl;
-    if (!find_tile<R>(a, g, blockIdx.x, lane, tl)) return;
+    make_tile<R>(a, g, cut.s, cut.tile, tl);
     const int n_rows = min(R, tl.rows - tl.row0);
     const int32_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);  // the most that a row of the tile sees
     const int32_t lim_first = row_limit(tl, g, tl.row0);
-    const int32_t chunk = chunk_of(lim_last, n_chunks, kFewUnit), c0 = z * chunk;
-    if (z > 0 && c0 >= lim_last) return;
-    const int32_t c1 = min(c0 + chunk, lim_last);
+    const int32_t chunk = chunk_of((int32_t)tl.seen, cut.n, kFewUnit);  // (a row may end before the last ones)
+    const int32_t c0 = (int32_t)min((int64_t)z * chunk, (int64_t)lim_last), c1 = min(c0 + chunk, lim_last);
 
-    // pages of this wave's half blocks, a lane each
-    const int32_t *table = a.kv.tables + tl.s * kv.table_stride;
-    int64_t base = 0;
-    float ks = 1.0f, vs = 1.0f;
-    bool valid = false;
+    // Q: this lane's column is term `t` of row `r`
+    const int t = col / R, r = col % R;
+    const bool live = t < NT && r < n_rows;
+    const int row = tl.row0 + min(r, n_rows - 1);
+    const int32_t lim = row_limit(tl, g, row);
+    Raw8<IO> qraw[2 * NK];
     {
-        const int32_t tok = c0 + ((lane >> 1) * kFewWaves + wave) * 32 + (lane & 1) * 16;
+        const int64_t off = (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head;
+#pragma unroll
+        for (int k = 0; k < 2 * NK; ++k) qraw[k] = load8<IO>(a.q, off + (k >> 1) * 64 + grp * 16 + (k & 1) * 8);
+    }
+
+    // pages of this wave's half blocks from token `from` on, a lane each
+    const int32_t *table = a.kv.tables + tl.s * kv.table_stride;
+    int64_t base;
+    float ks, vs;
+    uint64_t valid_mask;
+    auto look_up = [&](int32_t from) {
+        base = 0;
+        ks = vs = 1.0f;
+        bool valid = false;
+        const int64_t tok = (int64_t)from + ((lane >> 1) * kFewWaves + wave) * 32 + (lane & 1) * 16;
         if (tok < c1) {
             const int32_t page = table[tok >> kv.bs_shift];
             valid = page >= 0 && page < kv.num_blocks;
@@ -216,28 +374,13 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
             }
             base += (tok & (kv.block_size - 1)) * kv.c_tok + kvh * kv.c_head;
         }
-    }
-    const uint64_t valid_mask = __ballot(valid);
-
-    // Q's terms: this lane's column is term `t` of row `r`
-    const int t = col / R, r = col % R;
-    const bool live = t < NT && r < n_rows;
-    const int row = tl.row0 + min(r, n_rows - 1);
-    const int32_t lim = row_limit(tl, g, row);
-    bf16x8 qf[2 * NK];
-    {
-        const int64_t off = (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head;
-#pragma unroll
-        for (int k = 0; k < 2 * NK; ++k) {
-            float x[8];
-            unpack8<IO>(load8<IO>(a.q, off + (k >> 1) * 64 + grp * 16 + (k & 1) * 8), x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) qf[k][e] = (__bf16)(live ? term<NT>(x[e], t) : 0.0f);
-        }
-    }
-
-    const int n_blocks = (int)((c1 - c0 + 31) / 32);
-    const int n_mine = n_blocks > wave ? (n_blocks - wave + kFewWaves - 1) / kFewWaves : 0;
+        valid_mask = __ballot(valid);
+    };
+    auto blocks_of = [&](int32_t from) {  // of this wave, in the tokens looked up from there
+        const int n = (min(c1 - from, kFewPages) + 31) / 32;
+        return n > wave ? (n - wave + kFewWaves - 1) / kFewWaves : 0;
+    };
+    look_up(c0);
 
     u32x4 ka[NK], kb[NK];
     VRow<D> vr[8];
@@ -263,140 +406,160 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
         for (int j = 0; j < 8; ++j) vr[j] = load_vrow<D>(p + j * kv.c_tok);
     };
 
+    int n_mine = blocks_of(c0);
+    if (n_mine > 0) {
+        load_k(0);
+        load_v(0);
+    }
+    bf16x8 qf[2 * NK];
+#pragma unroll
+    for (int k = 0; k < 2 * NK; ++k) {
+        float x[8];
+        unpack8<IO>(qraw[k], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qf[k][e] = (__bf16)(live ? term<NT>(x[e], t) : 0.0f);
+    }
+
     float m = kNoMax, l = 0.0f;
     f32x4 o[ND];
 #pragma unroll
     for (int i = 0; i < ND; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    if (n_mine > 0) {
-        load_k(0);
-        load_v(0);
-    }
-    for (int it = 0; it < n_mine; ++it) {
-        const int32_t tok0 = c0 + (it * kFewWaves + wave) * 32;
-        const float ks0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks), 2 * it));
-        const float ks1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks), 2 * it + 1));
-        const float kscale = col < 8 ? ks0 : ks1;
-        const bool ok0 = (valid_mask >> (2 * it)) & 1, ok1 = (valid_mask >> (2 * it + 1)) & 1;
-        f32x4 sa = {0.0f, 0.0f, 0.0f, 0.0f}, sb = sa;
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u32x4 fa = {bf16_pair<false>(ka[k][2 * h], kscale), bf16_pair<true>(ka[k][2 * h], kscale),
-                                  bf16_pair<false>(ka[k][2 * h + 1], kscale), bf16_pair<true>(ka[k][2 * h + 1], kscale)};
-                const u32x4 fb = {bf16_pair<false>(kb[k][2 * h], kscale), bf16_pair<true>(kb[k][2 * h], kscale),
-                                  bf16_pair<false>(kb[k][2 * h + 1], kscale), bf16_pair<true>(kb[k][2 * h + 1], kscale)};
-                sa = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa), qf[2 * k + h], sa, 0, 0, 0);
-                sb = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb), qf[2 * k + h], sb, 0, 0, 0);
-            }
-        if (it + 1 < n_mine) load_k(it + 1);
-
-        // this lane: row r against tokens tok0 + 8*grp + 0..7
-        float p[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            p[j] = sum_terms<NT>(sa[j]) * a.scale_log2;
-            p[4 + j] = sum_terms<NT>(sb[j]) * a.scale_log2;
-        }
-        const bool ragged = tok0 + 32 > lim_first || !ok0 || !ok1;  // wave-uniform
-        const bool ok = grp < 2 ? ok0 : ok1;
-        const int32_t mine0 = tok0 + 8 * grp;
-        if (ragged) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (!ok || mine0 + j >= lim) p[j] = -__builtin_inff();
-        }
-        float mx = p[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) mx = fmaxf(mx, p[j]);
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        if (__any(mx > m)) {
-            const float m_new = fmaxf(m, mx);
-            const float f = __builtin_amdgcn_exp2f(m - m_new);
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < ND; ++i) o[i] *= f;
-            m = m_new;
-        }
-        uint32_t pf[4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            p[j] = __builtin_amdgcn_exp2f(p[j] - m);
-            l += p[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) pf[j] = pack16x2<kIoBF16>(term<NT>(p[2 * j], t), term<NT>(p[2 * j + 1], t));
-        const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{pf[0], pf[1], pf[2], pf[3]});
-
-        const float vs0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs), 2 * it));
-        const float vs1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs), 2 * it + 1));
-        const float vscale = grp < 2 ? vs0 : vs1;
-        bool nan = false;
-        if (ragged) {
-            // what no row of the tile sees may hold anything: it must not reach the product
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool off = !ok || mine0 + j >= lim_last;
-#pragma unroll
-                for (int w = 0; w < ND / 4; ++w) {
-                    if (off) vr[j].w[w] = 0;
-                    nan |= any_nan(vr[j].w[w]);
+    for (int32_t from = c0;;) {
+        for (int it = 0; it < n_mine; ++it) {
+            const int32_t tok0 = from + (it * kFewWaves + wave) * 32;
+            const float ks0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks), 2 * it));
+            const float ks1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks), 2 * it + 1));
+            const float kscale = col < 8 ? ks0 : ks1;
+            const bool ok0 = (valid_mask >> (2 * it)) & 1, ok1 = (valid_mask >> (2 * it + 1)) & 1;
+            f32x4 sa = {0.0f, 0.0f, 0.0f, 0.0f}, sb = sa;
+    #pragma unroll
+            for (int k = 0; k < NK; ++k)
+    #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 fa = {bf16_pair<false>(ka[k][2 * h], kscale), bf16_pair<true>(ka[k][2 * h], kscale),
+                                      bf16_pair<false>(ka[k][2 * h + 1], kscale), bf16_pair<true>(ka[k][2 * h + 1], kscale)};
+                    const u32x4 fb = {bf16_pair<false>(kb[k][2 * h], kscale), bf16_pair<true>(kb[k][2 * h], kscale),
+                                      bf16_pair<false>(kb[k][2 * h + 1], kscale), bf16_pair<true>(kb[k][2 * h + 1], kscale)};
+                    sa = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa), qf[2 * k + h], sa, 0, 0, 0);
+                    sb = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb), qf[2 * k + h], sb, 0, 0, 0);
                 }
-            }
-            nan = __any(nan);
-        }
-        uint32_t nan_vis[4];
-        if (nan) {  // rows that do see a NaN take it below; the others must not
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                nan_vis[j] = (ok && mine0 + 2 * j < lim ? 0x3f80u : 0u) | (ok && mine0 + 2 * j + 1 < lim ? 0x3f800000u : 0u);
-        }
-#pragma unroll
-        for (int w = 0; w < ND / 4; ++w) {
-            // bytes of two tokens side by side, then bf16 pairs (token 2j, token 2j + 1) of one dim
-            uint32_t lo[4], hi[4];
-#pragma unroll
+            if (it + 1 < n_mine) load_k(it + 1);
+
+            // this lane: row r against tokens tok0 + 8*grp + 0..7
+            float p[8];
+    #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                lo[j] = __builtin_amdgcn_perm(vr[2 * j + 1].w[w], vr[2 * j].w[w], 0x05010400u);
-                hi[j] = __builtin_amdgcn_perm(vr[2 * j + 1].w[w], vr[2 * j].w[w], 0x07030602u);
+                p[j] = sum_terms<NT>(sa[j]) * a.scale_log2;
+                p[4 + j] = sum_terms<NT>(sb[j]) * a.scale_log2;
             }
-            if (nan) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    u32x4 ind;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t &b = e < 2 ? lo[j] : hi[j];
-                        const int sh = (e & 1) * 16;
-                        const uint32_t x = b >> sh;
-                        const bool n0 = (x & 0x7fu) == 0x7fu, n1 = (x & 0x7f00u) == 0x7f00u;
-                        ind[j] = (n0 ? 0x3f80u : 0u) | (n1 ? 0x3f800000u : 0u);
-                        if (n0) b &= ~(0xffu << sh);
-                        if (n1) b &= ~(0xff00u << sh);
+            const bool ragged = tok0 + 32 > lim_first || !ok0 || !ok1;  // wave-uniform
+            const bool ok = grp < 2 ? ok0 : ok1;
+            const int32_t mine0 = tok0 + 8 * grp;
+            if (ragged) {
+    #pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (!ok || mine0 + j >= lim) p[j] = -__builtin_inff();
+            }
+            float mx = p[0];
+    #pragma unroll
+            for (int j = 1; j < 8; ++j) mx = fmaxf(mx, p[j]);
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            if (__any(mx > m)) {
+                const float m_new = fmaxf(m, mx);
+                const float f = __builtin_amdgcn_exp2f(m - m_new);
+                l *= f;
+    #pragma unroll
+                for (int i = 0; i < ND; ++i) o[i] *= f;
+                m = m_new;
+            }
+            uint32_t pf[4];
+    #pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                p[j] = __builtin_amdgcn_exp2f(p[j] - m);
+                l += p[j];
+            }
+    #pragma unroll
+            for (int j = 0; j < 4; ++j) pf[j] = pack16x2<kIoBF16>(term<NT>(p[2 * j], t), term<NT>(p[2 * j + 1], t));
+            const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{pf[0], pf[1], pf[2], pf[3]});
+
+            const float vs0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs), 2 * it));
+            const float vs1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs), 2 * it + 1));
+            const float vscale = grp < 2 ? vs0 : vs1;
+            bool nan = false;
+            if (ragged) {
+                // what no row of the tile sees may hold anything: it must not reach the product
+    #pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool off = !ok || mine0 + j >= lim_last;
+    #pragma unroll
+                    for (int w = 0; w < ND / 4; ++w) {
+                        if (off) vr[j].w[w] = 0;
+                        nan |= any_nan(vr[j].w[w]);
                     }
-                    const f32x4 cnt = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, ind),
-                        __builtin_bit_cast(bf16x8, u32x4{nan_vis[0], nan_vis[1], nan_vis[2], nan_vis[3]}),
-                        f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (cnt[q] > 0.0f) o[4 * w + e][q] = __builtin_nanf("");
                 }
+                nan = __any(nan);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                u32x4 fv;
-#pragma unroll
+            uint32_t nan_vis[4];
+            if (nan) {  // rows that do see a NaN take it below; the others must not
+    #pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    nan_vis[j] = (ok && mine0 + 2 * j < lim ? 0x3f80u : 0u) | (ok && mine0 + 2 * j + 1 < lim ? 0x3f800000u : 0u);
+            }
+    #pragma unroll
+            for (int w = 0; w < ND / 4; ++w) {
+                // bytes of two tokens side by side, then bf16 pairs (token 2j, token 2j + 1) of one dim
+                uint32_t lo[4], hi[4];
+    #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t b = e < 2 ? lo[j] : hi[j];
-                    fv[j] = e & 1 ? bf16_pair<true>(b, vscale) : bf16_pair<false>(b, vscale);
+                    lo[j] = __builtin_amdgcn_perm(vr[2 * j + 1].w[w], vr[2 * j].w[w], 0x05010400u);
+                    hi[j] = __builtin_amdgcn_perm(vr[2 * j + 1].w[w], vr[2 * j].w[w], 0x07030602u);
                 }
-                o[4 * w + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fv), pb, o[4 * w + e], 0, 0, 0);
+                if (nan) {
+    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        u32x4 ind;
+    #pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t &b = e < 2 ? lo[j] : hi[j];
+                            const int sh = (e & 1) * 16;
+                            const uint32_t x = b >> sh;
+                            const bool n0 = (x & 0x7fu) == 0x7fu, n1 = (x & 0x7f00u) == 0x7f00u;
+                            ind[j] = (n0 ? 0x3f80u : 0u) | (n1 ? 0x3f800000u : 0u);
+                            if (n0) b &= ~(0xffu << sh);
+                            if (n1) b &= ~(0xff00u << sh);
+                        }
+                        const f32x4 cnt = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, ind),
+                            __builtin_bit_cast(bf16x8, u32x4{nan_vis[0], nan_vis[1], nan_vis[2], nan_vis[3]}),
+                            f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+    #pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (cnt[q] > 0.0f) o[4 * w + e][q] = __builtin_nanf("");
+                    }
+                }
+    #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    u32x4 fv;
+    #pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t b = e < 2 ? lo[j] : hi[j];
+                        fv[j] = e & 1 ? bf16_pair<true>(b, vscale) : bf16_pair<false>(b, vscale);
+                    }
+                    o[4 * w + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fv), pb, o[4 * w + e], 0, 0, 0);
+                }
             }
+            if (it + 1 < n_mine) load_v(it + 1);
         }
-        if (it + 1 < n_mine) load_v(it + 1);
+        if (c1 - from <= kFewPages) break;
+        from += kFewPages;
+        look_up(from);
+        n_mine = blocks_of(from);
+        if (n_mine > 0) {
+            load_k(0);
+            load_v(0);
+        }
     }
 
     // the waves' parts meet in LDS
@@ -420,9 +583,9 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attend_few_kernel(Attend a,
         sml[wave][r][1] = l;
     }
     __syncthreads();
-    const bool whole = lim_last <= chunk;
-    Partial<D, R> *part = static_cast<Partial<D, R> *>(a.workspace) +
-                          (((int64_t)blockIdx.x * kv.nk + kvh) * n_chunks + z);
+    const bool whole = cut.n == 1;
+    Partial<D, R> *part = reinterpret_cast<Partial<D, R> *>(static_cast<char *>(a.workspace) + cut_list_bytes(p.max_cut)) +
+                          ((int64_t)(cut.slot + z) * kv.nk + kvh);
     for (int e = threadIdx.x; e < n_rows * (D / 8); e += 64 * kFewWaves) {
         const int rr = e / (D / 8), d = e % (D / 8) * 8;
         float mm = kNoMax, ll = 0.0f, y[8] = {};
@@ -1062,51 +1225,81 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     }
 }
 
-// Joins a tile's chunks: one workgroup a row, D/4 lanes over its dims and the rest over the chunks.
+// Joins a tile's chunks: one workgroup a row, D/4 lanes over its dims and the rest over the chunks.  The
+// largest maximum is found first, so the chunks' parts add up without waiting for one another.
+constexpr int kJoinThreads = 512;
+
 template <int IO, int D, int R>
-__global__ __launch_bounds__(256) void attend_join_kernel(Attend a, int n_chunks, int unit)
+__global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(Attend a, int n_chunks, int32_t max_cut)
 {
-    const int g = a.nq / a.kv.nk, kvh = blockIdx.y, rr = blockIdx.z;
+    constexpr int kWaves = kJoinThreads / 64, LANES = D / 4, PARTS = kJoinThreads / LANES, U = 4;
+    const int g = a.nq / a.kv.nk, kvh = blockIdx.y, rr = blockIdx.z, lane = threadIdx.x & 63;
     Tile tl;
-    if (!find_tile<R>(a, g, blockIdx.x, threadIdx.x & 63, tl)) return;
-    const int n_rows = min(R, tl.rows - tl.row0);
-    const int32_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);
-    const int32_t chunk = chunk_of(lim_last, n_chunks, unit);
-    if (rr >= n_rows || lim_last <= chunk) return;
-    const int n = (int)((lim_last + chunk - 1) / chunk);
-    const Partial<D, R> *part = static_cast<const Partial<D, R> *>(a.workspace) +
-                                ((int64_t)blockIdx.x * a.kv.nk + kvh) * n_chunks;
-    constexpr int LANES = D / 4, PARTS = 256 / LANES;
+    int n;
+    const Partial<D, R> *part;
+    int64_t stride = 1;  // from a chunk's part to the next one's
+    if constexpr (R == kManyRows) {
+        if (!find_tile<R>(a, g, blockIdx.x, lane, tl)) return;
+        const int32_t lim_last = row_limit(tl, g, min(tl.row0 + R, tl.rows) - 1);
+        const int32_t chunk = chunk_of(lim_last, n_chunks, kManyUnit);
+        if (lim_last <= chunk) return;
+        n = (int)((lim_last + chunk - 1) / chunk);
+        part = static_cast<const Partial<D, R> *>(a.workspace) + ((int64_t)blockIdx.x * a.kv.nk + kvh) * n_chunks;
+    } else {
+        const CutList *list = static_cast<const CutList *>(a.workspace);
+        if ((int64_t)blockIdx.x >= list->n) return;
+        const Cut c = list->cut[blockIdx.x];
+        make_tile<R>(a, g, c.s, c.tile, tl);
+        n = c.n;
+        part = reinterpret_cast<const Partial<D, R> *>(static_cast<const char *>(a.workspace) + cut_list_bytes(max_cut)) +
+               ((int64_t)c.slot * a.kv.nk + kvh);
+        stride = a.kv.nk;
+    }
+    if (rr >= tl.rows - tl.row0) return;
     const int d = threadIdx.x % LANES * 4, sub = threadIdx.x / LANES;
-    float m = kNoMax, l = 0.0f;
-    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int z = sub; z < n; z += PARTS) {
-        const float pm = part[z].ml[rr][0], pl = part[z].ml[rr][1];
-        const f32x4 po = *reinterpret_cast<const f32x4 *>(&part[z].o[rr][d]);
-        const float mn = fmaxf(m, pm), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(pm - mn);
-        l = l * f0 + pl * f1;
-        y = y * f0 + po * f1;
-        m = mn;
-    }
-    __shared__ float sm[PARTS][2];
+
+    __shared__ float sm[kWaves], sl[PARTS];
     __shared__ f32x4 sy[PARTS][LANES];
-    sy[sub][d / 4] = y;
-    if (d == 0) {
-        sm[sub][0] = m;
-        sm[sub][1] = l;
+    float m = kNoMax;
+    for (int z = threadIdx.x; z < n; z += kJoinThreads) m = fmaxf(m, part[z * stride].ml[rr][0]);
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
+    if (lane == 0) sm[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sm[w]);
+
+    float l = 0.0f;
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int z0 = sub; z0 < n; z0 += U * PARTS) {
+        f32x4 po[U];
+        float f[U], pl[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Partial<D, R> &p = part[min(z0 + u * PARTS, n - 1) * stride];
+            f[u] = p.ml[rr][0];
+            pl[u] = p.ml[rr][1];
+            po[u] = *reinterpret_cast<const f32x4 *>(&p.o[rr][d]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (z0 + u * PARTS >= n) break;
+            const float e = __builtin_amdgcn_exp2f(f[u] - m);
+            l += pl[u] * e;
+            y += po[u] * e;
+        }
     }
+    sy[sub][d / 4] = y;
+    if (d == 0) sl[sub] = l;
     __syncthreads();
     const int e = threadIdx.x;
     if (e >= D / 8) return;
-    float mm = kNoMax, ll = 0.0f, r[8] = {};
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) mm = fmaxf(mm, sm[p][0]);
+    float ll = 0.0f, r[8] = {};
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-        const float f = __builtin_amdgcn_exp2f(sm[p][0] - mm);
-        ll += sm[p][1] * f;
+        ll += sl[p];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] += sy[p][2 * e + (i >> 2)][i & 3] * f;
+        for (int i = 0; i < 8; ++i) r[i] += sy[p][2 * e + (i >> 2)][i & 3];
     }
     const int rw = tl.row0 + rr;
     const int64_t tok = tl.t0 + rw / g;
@@ -1116,37 +1309,52 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Attend a, int n_chunks
     for (int i = 0; i < 8; ++i) r[i] = ll == 0.0f ? 0.0f : r[i] * inv;
     store_out8<IO>(a, tok * a.o_tok + head * a.o_head + 8 * e, r);
     if (a.lse && e == 0)
-        a.lse[tok * a.nq + head] = ll == 0.0f ? -__builtin_inff() : 0.69314718055994531f * (mm + __log2f(ll));
+        a.lse[tok * a.nq + head] = ll == 0.0f ? -__builtin_inff() : 0.69314718055994531f * (m + __log2f(ll));
 }
 
 // ------------------------------------------------------------------ launchers ------------------
 struct Plan {
     bool many;
     int64_t tiles;
-    int rows;      // of a tile
-    int n_chunks;
-    size_t bytes;  // of the workspace
+    int rows;         // of a tile
+    int64_t grid;     // few rows: chunks at most
+    FewPlan few;
+    int n_chunks;     // many rows: of a tile
+    size_t bytes;     // of the workspace
 };
 
-// Tiles of many rows from this many rows a sequence and KV head on the average.
-constexpr int64_t kManyFrom = 16;
-// Workgroups wanted: the context is cut where the tiles alone are fewer.
-constexpr int64_t kFewFill = 2048, kManyFill = 512;
+// Tiles of many rows where a sequence's rows of a KV head would fill more than four tiles of few rows, which
+// read the cache once each.  Measured (us, few against many; bf16, 8 query and 2 KV heads of 256): 3
+// sequences with 20,000 tokens behind them, 16 rows each 30 / 35, 32 rows 38 / 36, 48 rows 79 / 43; 16
+// sequences with 1,500, 32 rows 28 / 36, 48 rows 45 / 40.  fp32 (4 rows a tile): 16 rows 44 / 69, 24 rows 89 / 70.
+constexpr int64_t kFewTiles = 4;
+// Workgroups wanted for many rows: the context is cut where the tiles alone are fewer.  One a compute unit
+// runs at once; twice as many took 57 us where these take 44 (3 sequences of 16 tokens behind 20,011).
+constexpr int64_t kManyFill = 256;
 
 Plan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io, bool one_token,
                int32_t table_width, int32_t block_size)
 {
     Plan p{};
     const int64_t g = nq / nk, cap = std::max<int64_t>(1, (int64_t)table_width * block_size);
-    p.many = n_tokens * g > kManyFrom * n_seqs;
-    p.rows = p.many ? kManyRows : (io == kIoF32 ? kRowsOf<3> : kRowsOf<2>);
+    const int few_rows = io == kIoF32 ? kRowsOf<3> : kRowsOf<2>;
+    p.many = n_tokens * g > kFewTiles * few_rows * n_seqs;
+    p.rows = p.many ? kManyRows : few_rows;
     p.tiles = one_token ? (int64_t)n_seqs * ((g + p.rows - 1) / p.rows) : n_tokens * g / p.rows + n_seqs;
-    const int64_t unit = p.many ? kManyUnit : kFewUnit, fill = p.many ? kManyFill : kFewFill;
-    const int64_t most = (cap + unit - 1) / unit;
-    int64_t n = std::min(most, std::max<int64_t>(1, fill / (p.tiles * nk)));
-    if (!p.many) n = std::max(n, (cap + kFewMost - 1) / kFewMost);
-    p.n_chunks = (int)n;
-    p.bytes = n > 1 ? (size_t)(p.tiles * nk * n) * (size_t)(p.rows * (head_dim + 2) * 4) : 0;
+    const int64_t unit = p.many ? kManyUnit : kFewUnit, most = (cap + unit - 1) / unit;
+    const size_t part = (size_t)(p.rows * (head_dim + 2) * 4) * nk;
+    if (p.many) {
+        p.n_chunks = (int)std::min(most, std::max<int64_t>(1, kManyFill / (p.tiles * nk)));
+        if (p.n_chunks > 1) p.bytes = part * (size_t)(p.tiles * p.n_chunks);
+        return p;
+    }
+    p.few.budget = std::max(1, 256 * few_resident(head_dim) / nk);
+    p.grid = std::min(p.tiles + p.few.budget, p.tiles * most);
+    if (most > 1) {
+        p.few.max_cut = (int32_t)std::min<int64_t>(p.tiles, p.few.budget);
+        p.few.max_slots = (int32_t)std::min<int64_t>(2 * p.few.budget, p.tiles * most);
+        p.bytes = cut_list_bytes(p.few.max_cut) + part * (size_t)p.few.max_slots;
+    }
     return p;
 }
 
@@ -1155,14 +1363,19 @@ hipError_t launch_attend_d(const Attend &a, hipStream_t stream)
 {
     constexpr int NT = IO == kIoF32 ? 3 : 2;
     const Plan p = make_plan(a.n_tokens, a.n_seqs, a.nq, a.kv.nk, D, IO, a.cu == nullptr, a.kv.table_width, a.kv.block_size);
-    const dim3 grid((unsigned)p.tiles, a.kv.nk, p.n_chunks);
-    if (p.many) attend_many_kernel<IO, D><<<grid, 64 * kManyWaves, 0, stream>>>(a, p.n_chunks);
-    else attend_few_kernel<IO, D, NT><<<grid, 64 * kFewWaves, 0, stream>>>(a, p.n_chunks);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.n_chunks == 1) return e;
-    const dim3 join((unsigned)p.tiles, a.kv.nk, p.rows);
-    if (p.many) attend_join_kernel<IO, D, kManyRows><<<join, 256, 0, stream>>>(a, p.n_chunks, kManyUnit);
-    else attend_join_kernel<IO, D, kRowsOf<NT>><<<join, 256, 0, stream>>>(a, p.n_chunks, kFewUnit);
+    const int32_t nk = a.kv.nk, g = a.nq / nk;
+    if (p.many) {
+        attend_many_kernel<IO, D><<<dim3((unsigned)p.tiles, nk, p.n_chunks), 64 * kManyWaves, 0, stream>>>(a, p.n_chunks);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || p.n_chunks == 1) return e;
+        attend_join_kernel<IO, D, kManyRows><<<dim3((unsigned)p.tiles, nk, kManyRows), kJoinThreads, 0, stream>>>(a, p.n_chunks, 0);
+    } else {
+        attend_few_kernel<IO, D, NT><<<dim3((unsigned)p.grid, nk), 64 * kFewWaves, 0, stream>>>(a, p.few);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || p.few.max_cut == 0) return e;
+        const int rows = a.cu ? p.rows : std::min(p.rows, g);
+        attend_join_kernel<IO, D, kRowsOf<NT>><<<dim3((unsigned)p.few.max_cut, nk, rows), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
+    }
     return hipGetLastError();
 }
 

@@ -261,7 +261,7 @@ mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_hea
     if (!aligned(lse, 4)) return fail(MROPE_ERR_ALIGN, "lse must be 4-byte aligned");
     // a tile has at least 4 rows and 256 threads
     const int64_t group = n_q_heads / n_kv_heads;
-    if ((n_tokens * ((group + 3) / 4) + n_seqs) * 256 > kMaxGridThreads)
+    if ((n_tokens * ((group + 3) / 4) + n_seqs + 1024) * 256 > kMaxGridThreads)
         return fail(MROPE_ERR_ARG, "too many query rows (%lld tokens, %d heads a KV head)", (long long)n_tokens, (int)group);
     if ((int64_t)table_width * block_size > kMaxContext)
         return fail(MROPE_ERR_ARG, "block_tables: at most 2^27 positions a sequence (got %lld)", (long long)table_width * block_size);

@@ -260,6 +260,44 @@ def test_attend_long(dtype, hq, hk, D, q_len):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_seqs,hq,hk,D", [(70, 8, 2, 64), (300, 6, 3, 128), (4300, 2, 1, 64)])
+def test_attend_uneven_batch(dtype, n_seqs, hq, hk, D):
+    """More sequences than lanes (and than lanes squared), contexts from none to thousands: the long ones
+    are cut, the short ones are not, and both kinds lie side by side in the batch."""
+    say("attend uneven", dtype, n_seqs, D)
+    g = torch.Generator().manual_seed(n_seqs)
+    ctx = torch.randint(0, 60, (n_seqs,), generator=g)
+    ctx[torch.randint(0, n_seqs, (9,), generator=g)] = torch.randint(1500, 6000, (9,), generator=g)
+    ctx[0], ctx[-1], ctx[n_seqs // 2] = 3001, 2500, 0
+    ctx = ctx.tolist()
+    w = World(ctx, 16, hk, D, seed=n_seqs)
+    check_attend(w, [1] * n_seqs, ctx, dtype, hq, one=True)
+    q_lens = [1 + (s % 3) if c else s % 2 for s, c in enumerate(ctx)]
+    check_attend(w, q_lens, ctx, dtype, hq, pad=3)
+
+
+@pytest.mark.parametrize("one", [True, False])
+def test_attend_long_chunks(one):
+    """So many KV heads and long sequences that a workgroup's chunk passes 4,096 tokens (its pages are
+    looked up again), on tables that name the same pages over and over."""
+    say("attend long chunks", one)
+    w = World([640], 16, 64, 64, seed=19)
+    ctx = [8900] * 7 + [70, 8889]
+    w.tables = w.tables[:, :40].repeat(9, 15)
+    w.tables[1] = w.tables[1].flip(0)
+    cu = list(range(10)) if one else [0, 2, 3, 4, 5, 6, 7, 8, 8, 11]
+    q = w.heads(cu[-1], 64, "bf16")
+    out, lse = mr.attend_kv8(q.cuda(), None if one else i32(cu).cuda(), i32(ctx).cuda(), w.tables.cuda(), *w.cache(), return_lse=True)
+    heads = [0, 31, 63]
+    part = [x[:, :, heads] for x in (w.kc, w.vc)] + [x[:, heads] for x in (w.ks, w.vs)]
+    o, z, spread, amp = ref.attend(q[:, heads], None if one else cu, ctx, w.tables.tolist(), *part, None)
+    ds = (3 * 64 + 8) * 2.0 ** -24 * amp
+    tol = HALF_STEP["bf16"] * o.abs() * 1.01 + (2 * ds[..., None] + KEPT["bf16"] + 2.0 ** -20 + 2 * 8900 * 2.0 ** -24) * spread + 1e-30
+    assert bool(((out[:, heads].cpu().double() - o).abs() <= tol).all())
+    assert bool(((lse[:, heads].cpu().double() - z).abs() <= ds + 8900 * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * z.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("q_len", [1, 6, 70])
 def test_attend_ignores_what_is_not_seen(dtype, q_len):
     """NaN codes, NaN and infinite scales, and bad page numbers wherever a row does not look; NaN in later
