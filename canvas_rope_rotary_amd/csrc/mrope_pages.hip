@@ -15,7 +15,6 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kPlan = 1024;  // threads of the plan kernels
-constexpr int kPer = 4;      // pages a thread ranks at a time
 constexpr int32_t kNotEnough = 1, kBadRow = 2;  // MROPE_PAGES_*
 
 // Exclusive prefix sum of v over the workgroup; total in `sum`.
@@ -44,25 +43,38 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t &sum)
 }
 
 // list[rank] = page for the pages of [from, to) with (refcount > 0) == live and rank < most; returns
-// how many there are below `most` or more (every page is counted until `most` are found).
+// how many there are below `most` or more (every page is counted until `most` are found).  A thread takes
+// kPer pages at a time: 16 where all of the pool is ranked, 4 where a few pages are wanted (pages are
+// few as well then, or the first thousands hold them).
+template <int kPer>
 __device__ int32_t rank_pages(const int32_t *ref, int32_t from, int32_t to, bool live, int32_t most, int32_t *list)
 {
     int32_t found = 0;
-    for (int64_t b = from; b < to && found < most; b += kPlan * kPer) {
+    const bool wide = reinterpret_cast<uintptr_t>(ref) % 16 == 0;
+    for (int64_t b = from / kPer * kPer; b < to && found < most; b += kPlan * kPer) {
+        const int64_t p0 = b + (int64_t)threadIdx.x * kPer;
         int32_t r[kPer], c = 0;
+        if (wide && p0 + kPer <= to) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int64_t p = b + (int64_t)threadIdx.x * kPer + i;
-            r[i] = p < to ? ref[p] : (live ? 0 : 1);
+            for (int i = 0; i < kPer; i += 4) {
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(ref + p0 + i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[i + e] = (int32_t)x[e];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) r[i] = p0 + i < to ? ref[p0 + i] : 0;
         }
+        uint32_t hit = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) c += (r[i] > 0) == live;
+        for (int i = 0; i < kPer; ++i) hit |= ((r[i] > 0) == live && p0 + i >= from && p0 + i < to ? 1u : 0u) << i;
+        c = __builtin_popcount(hit);
         int32_t sum;
         int32_t at = found + block_scan(c, sum);
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if ((r[i] > 0) == live) {
-                if (at < most) list[at] = (int32_t)(b + (int64_t)threadIdx.x * kPer + i);
+            if (hit >> i & 1) {
+                if (at < most) list[at] = (int32_t)(p0 + i);
                 ++at;
             }
         found += sum;
@@ -98,7 +110,7 @@ __device__ void plan_requests(const Pages &p, int32_t n, const PagesWs &ws, int3
         wanted += sum;
     }
     const int32_t most = (int32_t)min(wanted, (int64_t)p.num_blocks);
-    const int32_t found = min(rank_pages(p.refcount, 0, p.num_blocks, false, most, ws.list), most);
+    const int32_t found = min(rank_pages<4>(p.refcount, 0, p.num_blocks, false, most, ws.list), most);
     __syncthreads();
     for (int32_t i = threadIdx.x; i < n; i += kPlan) {
         int32_t st = 0;
@@ -201,14 +213,15 @@ __global__ __launch_bounds__(kPlan) void pages_fork_plan_kernel(Pages p, const i
 __global__ __launch_bounds__(kPlan) void pages_compact_plan_kernel(Pages p, int32_t *moved, PagesWs ws)
 {
     int32_t c = 0, live;
+#pragma unroll 8
     for (int64_t b = (int64_t)threadIdx.x; b < p.num_blocks; b += kPlan) {
         c += p.refcount[b] > 0;
         ws.remap[b] = (int32_t)b;
     }
     block_scan(c, live);
     // the i-th free page below `live` takes the i-th live page from there on: there are as many
-    const int32_t n = rank_pages(p.refcount, 0, live, false, p.num_blocks, ws.list);
-    rank_pages(p.refcount, live, p.num_blocks, true, p.num_blocks, ws.from);
+    const int32_t n = rank_pages<16>(p.refcount, 0, live, false, p.num_blocks, ws.list);
+    rank_pages<16>(p.refcount, live, p.num_blocks, true, p.num_blocks, ws.from);
     __syncthreads();
     for (int32_t i = threadIdx.x; i < n; i += kPlan) {
         const int32_t to = ws.list[i], from = ws.from[i];
@@ -219,26 +232,45 @@ __global__ __launch_bounds__(kPlan) void pages_compact_plan_kernel(Pages p, int3
     if (threadIdx.x == 0) ws.head[0] = *moved = n;
 }
 
+// Bytes [at, end) of a page by a wave, four loads on their way at a time.
 template <typename T>
-__device__ __forceinline__ void copy_span(char *to, const char *from, int64_t bytes)
+__device__ __forceinline__ void copy_span(char *to, const char *from, int64_t at, int64_t end)
 {
-    for (int64_t i = (int64_t)threadIdx.x * sizeof(T); i < bytes; i += 256 * (int64_t)sizeof(T))
-        *reinterpret_cast<T *>(to + i) = *reinterpret_cast<const T *>(from + i);
+    constexpr int U = 4, kStep = 64 * sizeof(T);
+    for (at += (threadIdx.x & 63) * sizeof(T); at < end; at += U * kStep) {
+        T x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (at + u * kStep < end) x[u] = *reinterpret_cast<const T *>(from + at + u * kStep);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (at + u * kStep < end) *reinterpret_cast<T *>(to + at + u * kStep) = x[u];
+    }
 }
 
-// Pages from[i] -> to[i] of every pool, a workgroup at a time.
+// Pages from[i] -> to[i] of every pool, pool after pool, a wave for kSpan bytes of a page: pages of a few
+// bytes (scales) do not hold a workgroup up, and large ones are shared out.
+constexpr int64_t kSpan = 4096;
+
 __device__ void copy_pages(const PoolSet &pools, int32_t num_blocks, const int32_t *from, const int32_t *to, int32_t n,
                            int64_t block, int64_t n_blocks)
 {
-    for (int64_t u = block; u < (int64_t)n * pools.n; u += n_blocks) {
-        const int32_t i = (int32_t)(u / pools.n), k = (int32_t)(u % pools.n);
-        const int32_t a = from[i], b = to[i];
-        if (a < 0 || a >= num_blocks || b < 0 || b >= num_blocks || a == b) continue;
-        char *dst = pools.ptr[k] + b * pools.stride[k];
-        const char *src = pools.ptr[k] + a * pools.stride[k];
-        if (pools.granule[k] == 16) copy_span<u32x4>(dst, src, pools.bytes[k]);
-        else if (pools.granule[k] == 4) copy_span<uint32_t>(dst, src, pools.bytes[k]);
-        else copy_span<uint8_t>(dst, src, pools.bytes[k]);
+    const int64_t waves = n_blocks * 4;
+    int64_t u = __builtin_amdgcn_readfirstlane((int)block * 4 + (threadIdx.x >> 6));
+    for (int k = 0; k < pools.n; ++k) {
+        const int64_t spans = (pools.bytes[k] + kSpan - 1) / kSpan, units = n * spans;
+        for (; u < units; u += waves) {
+            const int32_t i = (int32_t)(spans == 1 ? u : u / spans);
+            const int64_t at = (u - i * spans) * kSpan, end = min(at + kSpan, pools.bytes[k]);
+            const int32_t a = from[i], b = to[i];
+            if (a < 0 || a >= num_blocks || b < 0 || b >= num_blocks || a == b) continue;
+            char *dst = pools.ptr[k] + b * pools.stride[k];
+            const char *src = pools.ptr[k] + a * pools.stride[k];
+            if (pools.granule[k] == 16) copy_span<u32x4>(dst, src, at, end);
+            else if (pools.granule[k] == 4) copy_span<uint32_t>(dst, src, at, end);
+            else copy_span<uint8_t>(dst, src, at, end);
+        }
+        u -= units;  // the next pool's pages go on with the next wave
     }
 }
 
