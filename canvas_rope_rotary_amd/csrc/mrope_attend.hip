@@ -663,9 +663,27 @@ __device__ __forceinline__ f32x16 mfma16(u32x4 x, u32x4 y, f32x16 c)
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
 }
 
-// The output's sums stay in accumulation registers throughout: the compiler otherwise moved all of them
-// to the others and back in every tile, for the sake of a rescaling that few tiles do.
-__device__ __forceinline__ void keep_in_acc(f32x16 &x) { asm volatile("" : "+a"(x)); }
+// Workgroups of a compute unit that run at once.  For D = 256 a wave's sums and queries alone take 192 of
+// the 256 registers that two would leave it; for the others they hide one another's waits and
+// first and last steps.  Measured: 24 fp16 prompts of up to 900 tokens, D = 128, 189 us with one and 145
+// with two; four prompts of 1,500 tokens, D = 64, bf16 86, 82 and 69 us with one, two and three, fp32
+// 139 and 108 with one and two (for D = 128 it spills: 202 and 325).
+constexpr int many_resident(int io, int head_dim)
+{
+    if (head_dim == 256 || (io == kIoF32 && head_dim == 128)) return 1;
+    return head_dim == 64 && io != kIoF32 ? 3 : 2;
+}
+
+// The output's sums stay where they are throughout: the compiler otherwise moved all of them from the
+// accumulation registers to the others and back in every tile, for the sake of a rescaling that few
+// tiles do.  With more than one workgroup it halves the registers between the kinds as soon as any of the
+// accumulation registers is named, so there all are of the other kind.
+template <int IO, int D>
+__device__ __forceinline__ void pin(f32x16 &x)
+{
+    if constexpr (many_resident(IO, D) == 1) asm volatile("" : "+a"(x));
+    else asm volatile("" : "+v"(x));
+}
 
 // Eight e4m3 bytes in the 16-bit type (exact).
 template <int IO>
@@ -744,8 +762,70 @@ __device__ __forceinline__ i32x8 join8(u32x4 x, u32x4 y)
     return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
 }
 
+// Sum over the wave, in every lane.
+__device__ __forceinline__ int32_t wave_sum(int32_t x)
+{
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15 and :31
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
+// The tile of the rank-th longest context, and its number w: workgroups start in this order, so that a long
+// one does not begin when the others end (4 prompts of 1,500 tokens, bf16, D = 256: 117 us in the order
+// of the batch, 86 so; 8 of 4,096: 868 and 738).  Tile k of a sequence is ranked by past + floor(R (k + 1) / g); the rank-th
+// largest of these is searched for, a sequence a lane.  Batches of more sequences than lanes start from the last
+// tile: with so many the ends are small.
+template <int R>
+__device__ __forceinline__ bool find_long_tile(const Attend &a, int g, int64_t rank, int64_t n_tiles, int lane, Tile &t, int64_t &w)
+{
+    if (a.n_seqs > 64) {
+        w = n_tiles - 1 - rank;
+        return find_tile<R>(a, g, w, lane, t);
+    }
+    const bool in = lane < a.n_seqs;
+    const int32_t t0 = !in ? 0 : (a.cu ? a.cu[lane] : lane);
+    const int32_t len = !in ? 0 : (a.cu ? (int32_t)max(min((int64_t)a.cu[lane + 1], a.n_tokens) - t0, (int64_t)0) : 1);
+    const int32_t tiles = (int32_t)(((int64_t)len * g + R - 1) / R);
+    const int32_t past = in ? max(a.ctx[lane], 0) - len : 0;
+    if (rank >= wave_sum(tiles)) return false;
+    auto count = [&](int64_t x) {  // of the lane's tiles that are ranked by x or more: k + 1 >= (x - past) g / R
+        const int64_t k1 = ((x - past) * g + R - 1) >> __builtin_ctz(R);
+        return tiles - (int32_t)min(max(k1 - 1, (int64_t)0), (int64_t)tiles);
+    };
+    int32_t lo32 = tiles ? past : 0x7fffffff;
+    int32_t span = 0;  // of the ranks, from the least past on
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) lo32 = min(lo32, __shfl_xor(lo32, x));
+    if (tiles) span = (int32_t)min((int64_t)past - lo32 + (int64_t)R * tiles / g + 1, (int64_t)0x7fffffff);
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) span = max(span, __shfl_xor(span, x));
+    int64_t lo = __builtin_amdgcn_readfirstlane(lo32), hi = lo + __builtin_amdgcn_readfirstlane(span);
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (wave_sum(count(mid)) > rank) lo = mid;
+        else hi = mid;
+    }
+    const int32_t from = count(lo), longer = count(hi), same = from - longer;
+    int32_t up = same;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) {
+        const int32_t o = __shfl_up(up, x);
+        if (lane >= x) up += o;
+    }
+    const int32_t j = (int32_t)rank - wave_sum(longer);
+    const int s = __builtin_popcountll(__ballot(up <= j));
+    const int32_t k = __builtin_amdgcn_readlane(tiles - from + j - (up - same), s);
+    const int32_t at = __builtin_amdgcn_readlane(t0, s);
+    w = (a.cu ? (int64_t)at * g / R + s : (int64_t)s * ((g + R - 1) / R)) + k;
+    return make_tile<R>(a, g, s, at, __builtin_amdgcn_readlane(len, s), k, t);
+}
+
 template <int IO, int D>
-__global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, int n_chunks)
+__global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_many_kernel(Attend a, int n_chunks, int64_t all_tiles)
 {
     constexpr int QT = IO == kIoF32 ? 3 : 1;                          // 16-bit terms of Q
     constexpr int N = IO == kIoBF16 ? 2 : 3;                          // terms of P: e4m3, or bf16 for fp32
@@ -757,11 +837,11 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
     const Kv8 &kv = a.kv;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int col = lane & 31, half = lane >> 5;
-    const int g = a.nq / kv.nk, kvh = blockIdx.y, z = blockIdx.z;
+    const int g = a.nq / kv.nk, kvh = blockIdx.x % kv.nk, z = blockIdx.z;
 
     Tile tl;
-    const int64_t w = gridDim.x - 1 - blockIdx.x;  // a prompt's later tiles see more: they go first
-    if (!find_tile<kManyRows>(a, g, w, lane, tl)) return;
+    int64_t w;
+    if (!find_long_tile<kManyRows>(a, g, blockIdx.x / kv.nk, all_tiles, lane, tl, w)) return;
     const int n_rows = min(kManyRows, tl.rows - tl.row0);
     const int32_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);
     const int32_t chunk = chunk_of(lim_last, n_chunks, kManyUnit), c0 = z * chunk;
@@ -934,7 +1014,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
 #pragma unroll
         for (int q = 0; q < 16; ++q) o[i][q] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NO; ++i) keep_in_acc(o[i]);
+    for (int i = 0; i < NO; ++i) pin<IO, D>(o[i]);
 
     // P of the tile before, in terms: its product with V is taken while the next softmax runs
     u32x4 pf[N][PW];
@@ -999,7 +1079,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
 
         // The scores, step by step, their operands read kAhead steps before their use; beside them the
         // next tile goes to LDS, and the one after it is asked for.  (Past the last tile both are done for nobody.)
-        constexpr int kAhead = NS < 8 ? 2 : 4;
+        constexpr int kAhead = many_resident(IO, D) > 1 ? 2 : 4;
         const uint8_t *kb = &lds.k[it & 1][col][16 * half];
         auto key_piece = [&](int k, int h) { return *reinterpret_cast<const u32x4 *>(kb + h * 32 * (2 * D + 16) + k * 32); };
         f32x16 s[2];
@@ -1037,9 +1117,10 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
             ev[j] = lds.ev[it & 1][j];
             dead[j] = lds.dead[it & 1][j];
         }
-        u32x4 vx[3][2];  // V's operands, two products ahead
+        constexpr int kVAhead = many_resident(IO, D) > 1 ? 1 : 2;
+        u32x4 vx[kVAhead + 1][2];  // V's operands
 #pragma unroll
-        for (int i = 0; i < 2 && i < NO; ++i) {
+        for (int i = 0; i < kVAhead && i < NO; ++i) {
             vx[i][0] = value_piece(vprev, i, 0);
             vx[i][1] = value_piece(vprev, i, 1);
         }
@@ -1114,11 +1195,11 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
         };
 #pragma unroll
         for (int i = 0; i < NO; ++i) {
-            if (i + 2 < NO) {
-                vx[(i + 2) % 3][0] = value_piece(vprev, i + 2, 0);
-                vx[(i + 2) % 3][1] = value_piece(vprev, i + 2, 1);
+            if (i + kVAhead < NO) {
+                vx[(i + kVAhead) % (kVAhead + 1)][0] = value_piece(vprev, i + kVAhead, 0);
+                vx[(i + kVAhead) % (kVAhead + 1)][1] = value_piece(vprev, i + kVAhead, 1);
             }
-            value_product(i, vx[i % 3][0], vx[i % 3][1]);
+            value_product(i, vx[i % (kVAhead + 1)][0], vx[i % (kVAhead + 1)][1]);
             if (i == 0) begin();
 #pragma unroll
             for (int n = 0; n < 8; ++n)
@@ -1137,9 +1218,9 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
             l *= c;
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
-                keep_in_acc(o[i]);  // nor read before the branch
+                pin<IO, D>(o[i]);  // nor read before the branch
                 o[i] *= c;
-                keep_in_acc(o[i]);
+                pin<IO, D>(o[i]);
             }
             m = m_new;
         }
@@ -1150,7 +1231,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void attend_many_kernel(Attend a, 
 #pragma unroll
             for (int e = 0; e < PW; ++e) pf[n][e] = pn[n][e];
 #pragma unroll
-        for (int i = 0; i < NO; ++i) keep_in_acc(o[i]);
+        for (int i = 0; i < NO; ++i) pin<IO, D>(o[i]);
         if (nan_here) {  // rare: the dims in which this lane's row sees a NaN, half of them a lane
             const int32_t seen = lim - t0;
 #pragma unroll 1
@@ -1328,10 +1409,6 @@ struct Plan {
 // sequences with 20,000 tokens behind them, 16 rows each 30 / 35, 32 rows 38 / 36, 48 rows 79 / 43; 16
 // sequences with 1,500, 32 rows 28 / 36, 48 rows 45 / 40.  fp32 (4 rows a tile): 16 rows 44 / 69, 24 rows 89 / 70.
 constexpr int64_t kFewTiles = 4;
-// Workgroups wanted for many rows: the context is cut where the tiles alone are fewer.  One a compute unit
-// runs at once; twice as many took 57 us where these take 44 (3 sequences of 16 tokens behind 20,011).
-constexpr int64_t kManyFill = 256;
-
 Plan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io, bool one_token,
                int32_t table_width, int32_t block_size)
 {
@@ -1344,7 +1421,11 @@ Plan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t
     const int64_t unit = p.many ? kManyUnit : kFewUnit, most = (cap + unit - 1) / unit;
     const size_t part = (size_t)(p.rows * (head_dim + 2) * 4) * nk;
     if (p.many) {
-        p.n_chunks = (int)std::min(most, std::max<int64_t>(1, kManyFill / (p.tiles * nk)));
+        // The context is cut where the tiles are fewer than the compute units; twice as many chunks took 57 us
+        // where these take 44 (3 sequences of 16 tokens behind 20,011, bf16, D = 256), and two or three a
+        // compute unit, which D = 128 and 64 have room for, 46 and 40 us for 42 and 36 (2 of 300 behind 500).
+        const int64_t fill = 256;
+        p.n_chunks = (int)std::min(most, std::max<int64_t>(1, fill / (p.tiles * nk)));
         if (p.n_chunks > 1) p.bytes = part * (size_t)(p.tiles * p.n_chunks);
         return p;
     }
@@ -1365,7 +1446,7 @@ hipError_t launch_attend_d(const Attend &a, hipStream_t stream)
     const Plan p = make_plan(a.n_tokens, a.n_seqs, a.nq, a.kv.nk, D, IO, a.cu == nullptr, a.kv.table_width, a.kv.block_size);
     const int32_t nk = a.kv.nk, g = a.nq / nk;
     if (p.many) {
-        attend_many_kernel<IO, D><<<dim3((unsigned)p.tiles, nk, p.n_chunks), 64 * kManyWaves, 0, stream>>>(a, p.n_chunks);
+        attend_many_kernel<IO, D><<<dim3((unsigned)(p.tiles * nk), 1, p.n_chunks), 64 * kManyWaves, 0, stream>>>(a, p.n_chunks, p.tiles);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.n_chunks == 1) return e;
         attend_join_kernel<IO, D, kManyRows><<<dim3((unsigned)p.tiles, nk, kManyRows), kJoinThreads, 0, stream>>>(a, p.n_chunks, 0);
