@@ -1306,15 +1306,19 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
     }
 }
 
-// Joins a tile's chunks: one workgroup a row, D/4 lanes over its dims and the rest over the chunks.  The
-// largest maximum is found first, so the chunks' parts add up without waiting for one another.
-constexpr int kJoinThreads = 512;
+// Joins a tile's chunks: some waves a row, D/4 lanes over its dims and the rest over the chunks.  The
+// largest maximum is found first, so the chunks' parts add up without waiting for one another.  A row of many
+// chunks takes the eight waves of a workgroup, one of few chunks two (64 rows in 40 chunks: 6.0 us with
+// eight and 9.1 with two; 2 prompts of 300 tokens in six: 21.6 and 9.4).
+constexpr int kJoinThreads = 512, kJoinMany = 16;
 
-template <int IO, int D, int R>
+template <int IO, int D, int R, int ROWS>  // rows of a workgroup
 __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(Attend a, int n_chunks, int32_t max_cut)
 {
-    constexpr int kWaves = kJoinThreads / 64, LANES = D / 4, PARTS = kJoinThreads / LANES, U = 4;
-    const int g = a.nq / a.kv.nk, kvh = blockIdx.y, rr = blockIdx.z, lane = threadIdx.x & 63;
+    constexpr int kThreads = kJoinThreads / ROWS, kWaves = kThreads / 64;  // of a row
+    constexpr int LANES = D / 4, PARTS = kThreads / LANES, U = 4;
+    const int g = a.nq / a.kv.nk, kvh = blockIdx.y, lane = threadIdx.x & 63;
+    const int mine = threadIdx.x / kThreads, tid = threadIdx.x % kThreads, rr = blockIdx.z * ROWS + mine;
     Tile tl;
     int n;
     const Partial<D, R> *part;
@@ -1336,19 +1340,20 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(Attend a, int
                ((int64_t)c.slot * a.kv.nk + kvh);
         stride = a.kv.nk;
     }
-    if (rr >= tl.rows - tl.row0) return;
-    const int d = threadIdx.x % LANES * 4, sub = threadIdx.x / LANES;
+    const bool live = rr < min(R, tl.rows - tl.row0);
+    if (!live) n = 0;
+    const int d = tid % LANES * 4, sub = tid / LANES;
 
-    __shared__ float sm[kWaves], sl[PARTS];
-    __shared__ f32x4 sy[PARTS][LANES];
+    __shared__ float sm[ROWS][kWaves], sl[ROWS][PARTS];
+    __shared__ f32x4 sy[ROWS][PARTS][LANES];
     float m = kNoMax;
-    for (int z = threadIdx.x; z < n; z += kJoinThreads) m = fmaxf(m, part[z * stride].ml[rr][0]);
+    for (int z = tid; z < n; z += kThreads) m = fmaxf(m, part[z * stride].ml[rr][0]);
 #pragma unroll
     for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
-    if (lane == 0) sm[threadIdx.x >> 6] = m;
+    if (lane == 0) sm[mine][tid >> 6] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sm[w]);
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sm[mine][w]);
 
     float l = 0.0f;
     f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -1370,17 +1375,17 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(Attend a, int
             y += po[u] * e;
         }
     }
-    sy[sub][d / 4] = y;
-    if (d == 0) sl[sub] = l;
+    sy[mine][sub][d / 4] = y;
+    if (d == 0) sl[mine][sub] = l;
     __syncthreads();
-    const int e = threadIdx.x;
-    if (e >= D / 8) return;
+    const int e = tid;
+    if (!live || e >= D / 8) return;
     float ll = 0.0f, r[8] = {};
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-        ll += sl[p];
+        ll += sl[mine][p];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] += sy[p][2 * e + (i >> 2)][i & 3];
+        for (int i = 0; i < 8; ++i) r[i] += sy[mine][p][2 * e + (i >> 2)][i & 3];
     }
     const int rw = tl.row0 + rr;
     const int64_t tok = tl.t0 + rw / g;
@@ -1449,13 +1454,17 @@ hipError_t launch_attend_d(const Attend &a, hipStream_t stream)
         attend_many_kernel<IO, D><<<dim3((unsigned)(p.tiles * nk), 1, p.n_chunks), 64 * kManyWaves, 0, stream>>>(a, p.n_chunks, p.tiles);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.n_chunks == 1) return e;
-        attend_join_kernel<IO, D, kManyRows><<<dim3((unsigned)p.tiles, nk, kManyRows), kJoinThreads, 0, stream>>>(a, p.n_chunks, 0);
+        const unsigned tiles = (unsigned)p.tiles;
+        if (p.n_chunks > kJoinMany)
+            attend_join_kernel<IO, D, kManyRows, 1><<<dim3(tiles, nk, kManyRows), kJoinThreads, 0, stream>>>(a, p.n_chunks, 0);
+        else
+            attend_join_kernel<IO, D, kManyRows, 4><<<dim3(tiles, nk, kManyRows / 4), kJoinThreads, 0, stream>>>(a, p.n_chunks, 0);
     } else {
         attend_few_kernel<IO, D, NT><<<dim3((unsigned)p.grid, nk), 64 * kFewWaves, 0, stream>>>(a, p.few);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.few.max_cut == 0) return e;
         const int rows = a.cu ? p.rows : std::min(p.rows, g);
-        attend_join_kernel<IO, D, kRowsOf<NT>><<<dim3((unsigned)p.few.max_cut, nk, rows), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
+        attend_join_kernel<IO, D, kRowsOf<NT>, 1><<<dim3((unsigned)p.few.max_cut, nk, rows), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
     }
     return hipGetLastError();
 }
