@@ -12,7 +12,10 @@
 // layout of mrope_rotary.h, which the first eight lanes' K chunks share.
 //
 // Bound: HBM.  At 8 Q + 2 KV heads of 256 bf16 dims a token moves 2,048 B of Q (rotated dims, in and
-// out), 2,048 B of K and V in and 1,024 B out.
+// out), 2,048 B of K and V in and 1,024 B out.  Measured: 64 sequences of 4,096 tokens 271 us, 1,345 MB at
+// 4.97 TB/s (a dense copy reaches 6.5, the 16-bit cache write 6.07: the waves of a page wait for one another
+// between its largest value and its codes); 32 ragged fp32 sequences, 92 MB, 30 us.  Several pages a
+// workgroup, the next one's rows fetched ahead, took 395 us: fewer workgroups fit beside them.
 #include <algorithm>
 
 #include "mrope_kv8.h"
@@ -225,8 +228,8 @@ __global__ __launch_bounds__(BS * kRowLanes<D>) void append_kernel(Append a, Rot
 
 // One new token a sequence: a wave a sequence, four a workgroup.  The wave holds 64/LPR units (K or V of
 // a head) of its token at a time, and eight Q heads; a unit's largest magnitude is a reduction over its
-// lanes, so nothing meets in LDS.  Bound: latency (position -> page -> scale -> store).  With a page a
-// workgroup, as above, a 4,096-sequence step took 58 us, fifteen of sixteen rows idle.
+// lanes, so nothing meets in LDS.  Bound: latency (position -> page -> scale -> store): 4,096 sequences
+// 9.1 us, 21 MB.  With a page a workgroup, as above, they took 58 us, fifteen of sixteen rows idle.
 template <int IO, int D>
 __global__ __launch_bounds__(256) void append_one_kernel(Append a, Rotary rot)
 {

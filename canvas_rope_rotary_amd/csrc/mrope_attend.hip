@@ -107,7 +107,9 @@ __device__ __forceinline__ int32_t chunk_of(int32_t lim, int n_chunks, int unit)
 // keep P to 2^-16; three hold fp32.  The codes of K and V are exact in bf16, their scales (powers of
 // two) applied by the conversion.
 //
-// Bound: the cache's bytes, 2*D a token and KV head.
+// Bound: the cache's bytes, 2*D a token and KV head.  Measured, bf16, 8 query and 2 KV heads of 256: 64
+// sequences of 4,096 positions 44.8 us and 8 of 32,768 45.4, 269 MB at 6.0 and 5.9 TB/s (a plain read of that
+// size reaches 6.1), the join 4.7 and 5.7 us more; a matrix instruction is busy a tenth of the time.
 template <int NT>
 constexpr int kRowsOf = NT == 2 ? 8 : 4;
 constexpr int kFewWaves = 4;
@@ -216,11 +218,14 @@ __device__ __forceinline__ int32_t seen_of(const Attend &a, int32_t s, bool in)
     return in ? (int32_t)min((int64_t)max(a.ctx[s], 0), (int64_t)a.kv.table_width << a.kv.bs_shift) : 0;
 }
 
+// Of a tile that sees so many positions (< 2^28, as is the unit).
+__device__ __forceinline__ int32_t chunks(int32_t seen, int32_t unit) { return max((int32_t)((uint32_t)(seen + unit - 1) / (uint32_t)unit), 1); }
+
 struct Sums {  // of a range of sequences: chunks, tiles that are cut, chunks of those
     int32_t all, cut, slots;
     __device__ void add(int32_t tiles, int32_t seen, int32_t unit)
     {
-        const int32_t n = max((int32_t)(((int64_t)seen + unit - 1) / unit), 1);
+        const int32_t n = chunks(seen, unit);
         all += tiles * n;
         if (n > 1) cut += tiles, slots += tiles * n;
     }
@@ -254,7 +259,7 @@ __device__ __forceinline__ bool find_chunk(const Attend &a, int g, int64_t w, in
 #pragma unroll
     for (int x = 1; x < 64; x *= 2) total += __shfl_xor(total, x);
     const int64_t want = (total + budget - 1) / budget;
-    const int32_t unit = (int32_t)max(min((want + kFewUnit - 1) / kFewUnit * kFewUnit, (int64_t)1 << 30), (int64_t)kFewUnit);
+    const int32_t unit = (int32_t)max(min((want + kFewUnit - 1) / kFewUnit * kFewUnit, (int64_t)1 << 28), (int64_t)kFewUnit);
 
     Sums own = {};
     if (per == 1) {
@@ -294,7 +299,7 @@ __device__ __forceinline__ bool find_chunk(const Attend &a, int g, int64_t w, in
     }
     seen = __builtin_amdgcn_readlane(seen, at);
     c.s = s;
-    c.n = max((int32_t)(((int64_t)seen + unit - 1) / unit), 1);
+    c.n = chunks(seen, unit);
     const int32_t k = (int32_t)w - base.all;
     c.tile = k / c.n;
     z = k - c.tile * c.n;
@@ -624,9 +629,9 @@ __global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_ke
 //
 // S^T = K Q^T runs in 16 bits (32 x 32 x 16): the codes of K are exact in bf16 and fp16, so the queries'
 // own type is exact too and fp32 queries take three bf16 terms (each the nearest to what the terms before
-// it leave).  K is decoded once, on its way to LDS; its page scale joins the softmax's factor.  (The 8-bit instruction would take K undecoded, but sums a product's
-// 64 terms with some 13 bits below the largest: measured, the scores' sums then were off by 1e-6 of
-// themselves where 32 bits give 4e-8.)
+// it leave).  K is decoded once, on its way to LDS; its page scale joins the softmax's factor.  (The 8-bit
+// instruction would take K undecoded, but sums a product's 64 terms with some 13 bits below the largest:
+// measured, the scores' sums then were off by 1e-6 of themselves where 32 bits give 4e-8.)
 //
 // O^T = V^T P^T runs on the 8-bit instruction (32 x 32 x 64, twice the 16-bit rate) for the 16-bit types,
 // with V's codes as they lie and P as N e4m3 terms, each 2^4 finer than the last: two keep P to 2^-8
@@ -640,6 +645,12 @@ __global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_ke
 // LDS transposed in that order, four keys of a dim in a word; its 16-byte pieces are swapped by
 // (dim / 2) % 4 and 64 bytes left free every D/16 dims, which keeps the eight lanes of a read cycle and
 // the lanes of a write in different banks.  K's rows are 16 bytes longer for the same reason.
+//
+// Measured: 8 prompts of 4,096 tokens, bf16, 8 query and 2 KV heads of 256: 738 us, 0.75 PFLOP/s of the
+// products (550 GFLOP; a large bf16 product reaches 1.22 here, and the value product takes two terms at twice
+// the rate).  With one wave a SIMD a tile of 64 tokens takes some 5,000 cycles, of which the matrix
+// instructions need 2,048 and the other vector instructions 2,600: the bound is the issue of one wave and its
+// waits, and a second wave does not fit (192 registers of sums and queries).
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -986,7 +997,8 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
     // keys 4*vt..: tile half vt/8, eight-key group (vt/2)%4, lane half vt%2; the swap of pieces takes four values
     int vput[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) vput[e] = 16 * VB * vc + 16 * vc + 4 * (((vt & 1) * 2 + (vt >> 3)) ^ ((VB / 2 * vc + e) & 3)) + ((vt >> 1) & 3);
+    for (int e = 0; e < 4; ++e)
+        vput[e] = 16 * VB * vc + 16 * vc + 4 * (((vt & 1) * 2 + (vt >> 3)) ^ ((VB / 2 * vc + e) & 3)) + ((vt >> 1) & 3);
     constexpr int kSlices = KP + VB / 4;
     auto store_slice = [&](int n, int i, uint32_t *vbuf) {
         if (n < KP) {
@@ -1451,7 +1463,8 @@ hipError_t launch_attend_d(const Attend &a, hipStream_t stream)
     const Plan p = make_plan(a.n_tokens, a.n_seqs, a.nq, a.kv.nk, D, IO, a.cu == nullptr, a.kv.table_width, a.kv.block_size);
     const int32_t nk = a.kv.nk, g = a.nq / nk;
     if (p.many) {
-        attend_many_kernel<IO, D><<<dim3((unsigned)(p.tiles * nk), 1, p.n_chunks), 64 * kManyWaves, 0, stream>>>(a, p.n_chunks, p.tiles);
+        const dim3 grid((unsigned)(p.tiles * nk), 1, p.n_chunks);
+        attend_many_kernel<IO, D><<<grid, 64 * kManyWaves, 0, stream>>>(a, p.n_chunks, p.tiles);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.n_chunks == 1) return e;
         const unsigned tiles = (unsigned)p.tiles;
@@ -1464,7 +1477,8 @@ hipError_t launch_attend_d(const Attend &a, hipStream_t stream)
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.few.max_cut == 0) return e;
         const int rows = a.cu ? p.rows : std::min(p.rows, g);
-        attend_join_kernel<IO, D, kRowsOf<NT>, 1><<<dim3((unsigned)p.few.max_cut, nk, rows), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
+        const dim3 join((unsigned)p.few.max_cut, nk, rows);
+        attend_join_kernel<IO, D, kRowsOf<NT>, 1><<<join, kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
     }
     return hipGetLastError();
 }

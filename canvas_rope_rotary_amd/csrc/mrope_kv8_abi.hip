@@ -254,7 +254,8 @@ mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_hea
     if (n_seqs < 0) return fail(MROPE_ERR_ARG, "n_seqs < 0");
     if (n_seqs == 0 && n_tokens > 0) return fail(MROPE_ERR_ARG, "tokens given but no sequences");
     if (!cu_seqlens && n_tokens != n_seqs) return fail(MROPE_ERR_ARG, "without cu_seqlens there is one token a sequence");
-    if (!std::isfinite(softmax_scale)) return fail(MROPE_ERR_ARG, "softmax_scale must be finite");
+    const float scale_log2 = (float)(softmax_scale * 1.4426950408889634);
+    if (!std::isfinite(scale_log2)) return fail(MROPE_ERR_ARG, "softmax_scale must be finite (in fp32)");
     st = check_kv8(k_cache, v_cache, k_scale, v_scale, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
                    n_kv_heads, head_dim, block_tables, table_stride, table_width, n_seqs);
     if (st != MROPE_OK) return st;
@@ -275,6 +276,7 @@ mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_hea
         if (!aligned(workspace, 256)) return fail(MROPE_ERR_WORKSPACE, "workspace not 256-byte aligned");
         if (workspace_bytes < need) return fail(MROPE_ERR_WORKSPACE, "workspace too small (%zu < %zu)", workspace_bytes, need);
     }
+    if (out == q) return fail(MROPE_ERR_ARG, "out must not be q");
     Attend a{};
     a.q = q;
     a.out = out;
@@ -289,7 +291,7 @@ mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_hea
     a.cu = cu_seqlens;
     a.n_seqs = n_seqs;
     a.ctx = context_lens;
-    a.scale_log2 = (float)(softmax_scale * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     a.workspace = workspace;
     a.kv = make_kv8(k_cache, v_cache, k_scale, v_scale, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
                     n_kv_heads, block_tables, table_stride, table_width, block_size);

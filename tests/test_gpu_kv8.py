@@ -276,6 +276,21 @@ def test_attend_uneven_batch(dtype, n_seqs, hq, hk, D):
     check_attend(w, q_lens, ctx, dtype, hq, pad=3)
 
 
+@pytest.mark.parametrize("dtype,D,n_seqs", [("bf16", 256, 64), ("f16", 64, 65), ("bf16", 128, 130), ("f32", 64, 7)])
+def test_attend_many_prompts(dtype, D, n_seqs):
+    """Prompts by the length of their contexts (up to as many sequences as lanes) and in the batch's order
+    (more), some of one token or none, some on a cache, some with fewer positions than tokens."""
+    say("attend many prompts", dtype, D, n_seqs)
+    g = torch.Generator().manual_seed(n_seqs)
+    q_lens = torch.randint(5, 45, (n_seqs,), generator=g).tolist()
+    q_lens[1], q_lens[2], q_lens[n_seqs // 2], q_lens[-1] = 0, 1, 130, 77
+    past = [int(x) for x in torch.randint(0, 90, (n_seqs,), generator=g)]
+    past[3], past[4] = -3, 700
+    ctx = [max(a + b, 0) for a, b in zip(q_lens, past)]
+    w = World(ctx, 32, 2, D, seed=n_seqs + D)
+    check_attend(w, q_lens, ctx, dtype, 12, pad=9)
+
+
 @pytest.mark.parametrize("one", [True, False])
 def test_attend_long_chunks(one):
     """So many KV heads and long sequences that a workgroup's chunk passes 4,096 tokens (its pages are

@@ -81,6 +81,14 @@ def test_attend_kv8_refusals(lib, kw, code):
     assert _attend(lib, **kw) == code
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(out=A), ARG), (dict(out=2 * A, sc=1e300), ARG), (dict(out=2 * A, sc=-3e38), ARG), (dict(out=2 * A, ws=None, tw=1 << 12, ts=1 << 12), WS),
+    (dict(out=2 * A, n=100, ns=1 << 19, nq=64, nk=64, kh=256, ct=1 << 14, qt=1 << 14, ot=1 << 14), ARG),
+])
+def test_attend_kv8_refusals_in_place_and_out_of_range(lib, kw, code):
+    assert _attend(lib, **kw) == code
+
+
 def test_kv8_nothing_to_do(lib):
     assert _apply(lib, n=0, ns=0, cu=None, planes=None) == OK
     assert _decode(lib, ns=0) == OK
