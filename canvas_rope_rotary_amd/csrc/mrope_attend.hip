@@ -329,18 +329,23 @@ __global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_ke
     const int col = lane & 15, grp = lane >> 4;
     const int g = a.nq / kv.nk, kvh = blockIdx.y;
 
-    Cut cut;
-    int32_t z, rank, n_cut;
-    CutList *list = static_cast<CutList *>(a.workspace);
-    const bool found = find_chunk<R>(a, g, blockIdx.x, p.budget, lane, cut, z, rank, n_cut);
-    if (p.max_cut > 0 && blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) list->n = min(n_cut, p.max_cut);
-    if (!found) return;
-    if (cut.n > 1) {
-        if (rank >= p.max_cut || cut.slot + cut.n > p.max_slots) return;  // (not for offsets that grow)
-        if (z == 0 && kvh == 0 && threadIdx.x == 0) list->cut[rank] = cut;
-    }
+    Cut cut = {0, 0, 0, 1};
+    int32_t z = 0;
     Tile tl;
-    make_tile<R>(a, g, cut.s, cut.tile, tl);
+    if (p.max_cut == 0) {  // tables of one chunk
+        if (!find_tile<R>(a, g, blockIdx.x, lane, tl)) return;
+    } else {
+        CutList *list = static_cast<CutList *>(a.workspace);
+        int32_t rank, n_cut;
+        const bool found = find_chunk<R>(a, g, blockIdx.x, p.budget, lane, cut, z, rank, n_cut);
+        if (blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) list->n = min(n_cut, p.max_cut);
+        if (!found) return;
+        if (cut.n > 1) {
+            if (rank >= p.max_cut || cut.slot + cut.n > p.max_slots) return;  // (not for offsets that grow)
+            if (z == 0 && kvh == 0 && threadIdx.x == 0) list->cut[rank] = cut;
+        }
+        make_tile<R>(a, g, cut.s, cut.tile, tl);
+    }
     const int n_rows = min(R, tl.rows - tl.row0);
     const int32_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);  // the most that a row of the tile sees
     const int32_t lim_first = row_limit(tl, g, tl.row0);
