@@ -655,7 +655,8 @@ __global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_ke
 // products (550 GFLOP; a large bf16 product reaches 1.22 here, and the value product takes two terms at twice
 // the rate).  With one wave a SIMD a tile of 64 tokens takes some 5,000 cycles, of which the matrix
 // instructions need 2,048 and the other vector instructions 2,600: the bound is the issue of one wave and its
-// waits, and a second wave does not fit (192 registers of sums and queries).
+// waits, and a second wave does not fit (192 registers of sums and queries).  Two waves that share 32 rows, each
+// with half of the keys and of the dims, took 769 us: they do the same step at the same time.
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
