@@ -101,6 +101,34 @@ def test_pages_large_pool():
     assert mr.pages_compact(*d.state, d.pools).item() == d.m.compact(d.host) == 0
 
 
+@pytest.mark.parametrize("n_pages,offset", [(20011, 1), (16384, 0), (16401, 3)])
+def test_pages_unaligned_counts_and_large_pages(n_pages, offset):
+    """Counts that begin off a 16-byte boundary, pools of odd sizes, pages of several spans next to pages of
+    a few bytes, a pool that needs the byte path."""
+    say("pages unaligned", n_pages, offset)
+    r = random.Random(n_pages)
+    d = Dev(n_pages, 50, 600, 16, 5)
+    store = torch.zeros(n_pages + 8, dtype=torch.int32, device="cuda")
+    d.refcount = store[offset:offset + n_pages]
+    d.host = [torch.randint(0, 250, (n_pages, n), dtype=torch.uint8) for n in (8, 5001, 1)]
+    d.pools = [x.cuda() for x in d.host]
+    for step in range(4):
+        rows = list(range(50))
+        lens = [r.randrange(0, 9000) for _ in rows]
+        assert mr.pages_grow(*d.state, i32(rows), i32(lens), 16).tolist() == d.m.grow(rows, lens), step
+        gone = r.sample(rows, 30)
+        mr.pages_free(*d.state, i32(gone))
+        d.m.free(gone)
+        src = [x for x in rows if x not in gone][:6]
+        got = mr.pages_fork(*d.state, i32(src), i32(gone[:6]), 16, d.pools)
+        assert got.tolist() == d.m.fork(src, gone[:6], d.host), step
+        mr.pages_free(*d.state, i32(src))
+        d.m.free(src)
+        assert int(mr.pages_compact(*d.state, d.pools)) == d.m.compact(d.host), step
+        d.check(step)
+    assert int(store[:offset].abs().sum()) == 0 and int(store[offset + n_pages:].abs().sum()) == 0
+
+
 def test_pages_shortage_in_order():
     d = Dev(10, 5, 10, 4, 2)
     rows, lens = [0, 1, 2, 3, 4], [8, 20, 16, 0, 4]  # 2, 5, 4 (too many), 0, 1 (behind it)
