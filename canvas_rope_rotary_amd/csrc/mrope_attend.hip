@@ -219,7 +219,10 @@ __device__ __forceinline__ int32_t seen_of(const Attend &a, int32_t s, bool in)
 }
 
 // Of a tile that sees so many positions (< 2^28, as is the unit).
-__device__ __forceinline__ int32_t chunks(int32_t seen, int32_t unit) { return max((int32_t)((uint32_t)(seen + unit - 1) / (uint32_t)unit), 1); }
+__device__ __forceinline__ int32_t chunks(int32_t seen, int32_t unit)
+{
+    return max((int32_t)((uint32_t)(seen + unit - 1) / (uint32_t)unit), 1);
+}
 
 struct Sums {  // of a range of sequences: chunks, tiles that are cut, chunks of those
     int32_t all, cut, slots;
@@ -653,8 +656,8 @@ __global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_ke
 //
 // Measured: 8 prompts of 4,096 tokens, bf16, 8 query and 2 KV heads of 256: 738 us, 0.75 PFLOP/s of the
 // products (550 GFLOP; a large bf16 product reaches 1.22 here, and the value product takes two terms at twice
-// the rate).  With one wave a SIMD a tile of 64 tokens takes some 5,000 cycles, of which the matrix
-// instructions need 2,048 and the other vector instructions 2,600: the bound is the issue of one wave and its
+// the rate).  With one wave a SIMD a tile of 64 tokens takes some 6,500 cycles (first and last steps
+// included), of which the matrix instructions need 2,048 and the other vector instructions 2,700: the bound is the issue of one wave and its
 // waits, and a second wave does not fit (192 registers of sums and queries).  Two waves that share 32 rows, each
 // with half of the keys and of the dims, took 769 us: they do the same step at the same time.
 typedef int i32x8 __attribute__((ext_vector_type(8)));
