@@ -14,7 +14,7 @@
 // Bound: HBM.  At 8 Q + 2 KV heads of 256 bf16 dims a token moves 2,048 B of Q (rotated dims, in and
 // out), 2,048 B of K and V in and 1,024 B out.  Measured: 64 sequences of 4,096 tokens 271 us, 1,345 MB at
 // 4.97 TB/s (a dense copy reaches 6.5, the 16-bit cache write 6.07: the waves of a page wait for one another
-// between its largest value and its codes); 32 ragged fp32 sequences, 92 MB, 28 us.  Several pages a
+// between its largest value and its codes); 37 ragged fp32 sequences, 92 MB, 28 us.  Several pages a
 // workgroup, the next one's rows fetched ahead, took 395 us: fewer workgroups fit beside them.
 #include <algorithm>
 
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(BS * kRowLanes<D>) void append_kernel(Append a, Rot
     constexpr int NV = D / 8 / LPR;               // chunks of 8 dims a lane holds of a row
     constexpr int kWaves = BS * LPR / 64;
     // (K or V, head) units held at a time: 1,024 threads have 128 registers; in fp32 four take 32.4 us and two
-    // 30.5 on the 32 ragged sequences, in bf16 there is no difference
+    // 30.5 on the 37 ragged sequences, in bf16 there is no difference
     constexpr int kUnits = kWaves > 8 || IO == kIoF32 ? 2 : 4;
     const Kv8 &kv = a.kv;
     const int lane = threadIdx.x & 63;
