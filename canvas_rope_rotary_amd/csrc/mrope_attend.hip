@@ -857,11 +857,15 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
     const Kv8 &kv = a.kv;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int col = lane & 31, half = lane >> 5;
-    const int g = a.nq / kv.nk, kvh = blockIdx.x % kv.nk, z = blockIdx.z;
+    // chunks vary fastest: neighbouring workgroups go to the eight dies in turn, and the tiles that are not
+    // there (the grid has room for more) come last
+    const int z = (int)(blockIdx.x % (unsigned)n_chunks);
+    const unsigned unit = blockIdx.x / (unsigned)n_chunks;
+    const int g = a.nq / kv.nk, kvh = unit % kv.nk;
 
     Tile tl;
     int64_t w;
-    if (!find_long_tile<kManyRows>(a, g, blockIdx.x / kv.nk, all_tiles, lane, tl, w)) return;
+    if (!find_long_tile<kManyRows>(a, g, unit / kv.nk, all_tiles, lane, tl, w)) return;
     const int n_rows = min(kManyRows, tl.rows - tl.row0);
     const int32_t lim_last = row_limit(tl, g, tl.row0 + n_rows - 1);
     const int32_t chunk = chunk_of(lim_last, n_chunks, kManyUnit), c0 = z * chunk;
@@ -1450,8 +1454,10 @@ Plan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t
         // The context is cut where the tiles are fewer than the compute units; twice as many chunks took 57 us
         // where these take 44 (3 sequences of 16 tokens behind 20,011, bf16, D = 256), and two or three a
         // compute unit, which D = 128 and 64 have room for, 46 and 40 us for 42 and 36 (2 of 300 behind 500).
-        const int64_t fill = 256;
-        p.n_chunks = (int)std::min(most, std::max<int64_t>(1, fill / (p.tiles * nk)));
+        // (Of the tiles in the grid those are counted that sequences of equal lengths would have.)
+        const int64_t fill = 256, seq_rows = (n_tokens * g + n_seqs - 1) / n_seqs;
+        const int64_t likely = std::min(p.tiles, n_seqs * ((seq_rows + p.rows - 1) / p.rows));
+        p.n_chunks = (int)std::min(most, std::max<int64_t>(1, fill / (likely * nk)));
         if (p.n_chunks > 1) p.bytes = part * (size_t)(p.tiles * p.n_chunks);
         return p;
     }
@@ -1472,7 +1478,7 @@ hipError_t launch_attend_d(const Attend &a, hipStream_t stream)
     const Plan p = make_plan(a.n_tokens, a.n_seqs, a.nq, a.kv.nk, D, IO, a.cu == nullptr, a.kv.table_width, a.kv.block_size);
     const int32_t nk = a.kv.nk, g = a.nq / nk;
     if (p.many) {
-        const dim3 grid((unsigned)(p.tiles * nk), 1, p.n_chunks);
+        const dim3 grid((unsigned)(p.tiles * nk * p.n_chunks));
         attend_many_kernel<IO, D><<<grid, 64 * kManyWaves, 0, stream>>>(a, p.n_chunks, p.tiles);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.n_chunks == 1) return e;
