@@ -635,43 +635,37 @@ __global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_ke
 // ------------------------------------------------------------------ many rows ------------------
 // One workgroup: 128 rows (32 a wave) against the context, 64 tokens at a time through LDS.
 //
-// S^T = K Q^T runs in 16 bits (32 x 32 x 16): the codes of K are exact in bf16 and fp16, so the queries'
-// own type is exact too and fp32 queries take three bf16 terms (each the nearest to what the terms before
-// it leave).  K is decoded once, on its way to LDS; its page scale joins the softmax's factor.  (The 8-bit
-// instruction would take K undecoded, but sums a product's 64 terms with some 13 bits below the largest:
-// measured, the scores' sums then were off by 1e-6 of themselves where 32 bits give 4e-8.)
+// Both products run in 16 bits (32 x 32 x 16).  S^T = K Q^T: the codes of K are exact in bf16 and fp16, so
+// the queries' own type is exact too and fp32 queries take three bf16 terms (each the nearest to what the
+// terms before it leave).  K is decoded once, on its way to LDS; its page scale joins the softmax's factor.
+// (The 8-bit instruction would take K undecoded, but sums a product's 64 terms with some 13 bits below the
+// largest: measured, the scores' sums then were off by 1e-6 of themselves where 32 bits give 4e-8.)
 //
-// O^T = V^T P^T runs on the 8-bit instruction (32 x 32 x 64, twice the 16-bit rate) for the 16-bit types,
-// with V's codes as they lie and P as N e4m3 terms, each 2^4 finer than the last: two keep P to 2^-8
-// (bf16's own rounding) at the price of one bf16 product, three keep fp16's.  V's page scale multiplies
-// P, and a tile's probabilities of a row are written under the power of two of the largest of them (the
-// instruction's block scale), so a row that lives on small pages, or far below its running maximum,
-// keeps its precision.  fp32 takes three bf16 terms of P and decodes V's operands.
+// O^T = V^T P^T: V is decoded, its page scale included, on its way to LDS (a code times a power of two is exact
+// in bf16), and P taken in bf16 terms: two keep it to 2^-17 for the 16-bit types, as the kernel for few rows
+// does, three keep fp32's 2^-24.  One term less would make the errors of the output's rounding visibly larger
+// (two e4m3 terms on the 8-bit instruction, 2^-8, took 16 % less time for heads of 256 and raised the error of a
+// bf16 output against 64 bits from 0.00165 to 0.00174).
 //
 // As in the kernel for few rows S^T leaves a lane with the scores of one row, here for 32 of the 64 keys,
-// and O^T takes them from there: key 32t + 8a + 4h + b is byte 16t + 4a + b of lane half h.  V goes to
-// LDS transposed in that order, four keys of a dim in a word; its 16-byte pieces are swapped by
-// (dim / 2) % 4 and 64 bytes left free every D/16 dims, which keeps the eight lanes of a read cycle and
-// the lanes of a write in different banks.  K's rows are 16 bytes longer for the same reason.
+// and O^T takes them from there: a step of 16 keys takes 8*a + 4*h + b, a < 2, b < 4, of lane half h.  V goes to
+// LDS transposed in that order, a dim's 64 keys in 128 bytes; its 16-byte pieces are swapped by the dim
+// (vswap) and 128 bytes left free every D/16 dims, which keeps the lanes of a read cycle and of a write in
+// different banks.  K's rows are 16 bytes longer for the same reason.  V is written a tile later than K, while
+// the scores of its own tile are taken, and read in the next: two buffers of each are enough.
 //
-// Measured: 8 prompts of 4,096 tokens, bf16, 8 query and 2 KV heads of 256: 738 us, 0.75 PFLOP/s of the
-// products (550 GFLOP; a large bf16 product reaches 1.22 here, and the value product takes two terms at twice
-// the rate).  With one wave a SIMD a tile of 64 tokens takes some 6,500 cycles (first and last steps
-// included), of which the matrix instructions need 2,048 and the other vector instructions 2,700: the bound is the issue of one wave and its
-// waits, and a second wave does not fit (192 registers of sums and queries).  Two waves that share 32 rows, each
-// with half of the keys and of the dims, took 769 us: they do the same step at the same time.
-typedef int i32x8 __attribute__((ext_vector_type(8)));
+// Measured: 8 prompts of 4,096 tokens, bf16, 8 query and 2 KV heads of 256: 871 us, 0.63 PFLOP/s (550 GFLOP; with
+// the second term of P the matrix instructions do 825, 0.95 PFLOP/s, where a large bf16 product reaches 1.22
+// here).  With one wave a SIMD a tile of 64 tokens takes some 7,100 cycles (first and last steps included), of
+// which the matrix instructions need 3,456: without the softmax's arithmetic it took 807 us, without the
+// reads of V 843, without its staging 812, with one term of P 734.  A second wave does not fit (192 registers
+// of sums and queries).
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kManyWaves = 4;
 constexpr int kManyRows = 32 * kManyWaves;
 constexpr int kManyUnit = 64;  // tokens of a tile
-
-__device__ __forceinline__ f32x16 mfma8(i32x8 x, i32x8 y, f32x16 c, int sx, int sy)
-{
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 0, 0, 0, sx, 0, sy);
-}
 
 // A product in 16 bits: fp16 for fp16 queries, else bf16.
 template <int IO>
@@ -685,13 +679,13 @@ __device__ __forceinline__ f32x16 mfma16(u32x4 x, u32x4 y, f32x16 c)
 
 // Workgroups of a compute unit that run at once.  For D = 256 a wave's sums and queries alone take 192 of
 // the 256 registers that two would leave it; for the others they hide one another's waits and
-// first and last steps.  Measured: 24 fp16 prompts of up to 900 tokens, D = 128, 189 us with one and 145
-// with two; four prompts of 1,500 tokens, D = 64, bf16 86, 82 and 69 us with one, two and three, fp32
-// 139 and 108 with one and two (for D = 128 it spills: 202 and 325).
+// first and last steps.  Measured: 24 fp16 prompts of up to 900 tokens, D = 128, 176 us with one and 131
+// with two; four prompts of 1,500 tokens, D = 64, bf16 47, 42 and 84 us with one, two and three (three
+// spill), fp32 57 with one and two; fp32, D = 128, 80 with one and 190 with two (spills).
 constexpr int many_resident(int io, int head_dim)
 {
     if (head_dim == 256 || (io == kIoF32 && head_dim == 128)) return 1;
-    return head_dim == 64 && io != kIoF32 ? 3 : 2;
+    return 2;
 }
 
 // The output's sums stay where they are throughout: the compiler otherwise moved all of them from the
@@ -705,7 +699,7 @@ __device__ __forceinline__ void pin(f32x16 &x)
     else asm volatile("" : "+v"(x));
 }
 
-// Eight e4m3 bytes in the 16-bit type (exact).
+// Eight e4m3 bytes in the 16-bit type (exact). 
 template <int IO>
 __device__ __forceinline__ u32x4 decode8(uint32_t u, uint32_t v)
 {
@@ -718,48 +712,27 @@ __device__ __forceinline__ u32x4 decode8(uint32_t u, uint32_t v)
         return u32x4{bf16_pair<false>(u, 1.0f), bf16_pair<true>(u, 1.0f), bf16_pair<false>(v, 1.0f), bf16_pair<true>(v, 1.0f)};
 }
 
-// Four values to N terms of four codes each; all but the first are coded 2^4 finer than the one before.
-template <int N>
-__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t (&t)[N])
-{
-    typedef short i16x2 __attribute__((ext_vector_type(2)));
-    t[0] = pack_e4m3(a, b, c, d);
-    float finer = 1.0f;
-#pragma unroll
-    for (int i = 1; i < N; ++i) {
-        const kv8_f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)t[i - 1], false);
-        const kv8_f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)t[i - 1], true);
-        a -= lo[0] * finer;
-        b -= lo[1] * finer;
-        c -= hi[0] * finer;
-        d -= hi[1] * finer;
-        finer *= 0.0625f;  // the conversion divides by it
-        i16x2 w = {0, 0};
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, finer, false);
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, finer, true);
-        t[i] = __builtin_bit_cast(uint32_t, w);
-    }
-}
-
 template <int D>
 constexpr int kVB = D / 16;  // dims of V a thread transposes, for four keys
 
 template <int D>
 struct alignas(16) ManyLds {
     uint8_t k[2][64][2 * D + 16];       // 16-bit keys
-    uint32_t v[3][16 * (D + 16)];       // word of (dim d, keys 4w..): see vword()
+    uint8_t v[2][128 * (D + 16)];       // bf16, a dim's 64 keys side by side: see vbyte()
     uint8_t nanv[2][16][D];             // bit b of [w][d]: key 4w + b has a NaN in dim d (written where a row may not see it)
     uint32_t bad[kManyRows][D / 32];    // bit d of a row: it saw a NaN in that dim of V
     int32_t any_bad;
-    int32_t nan[2];                     // 1 + the last tile in which `nanv` has a bit
-    float ks[2][4], ev[2][4];           // by 16 keys: K's scale, the exponent of V's
+    int32_t nan[2];                     // the last tile in which `nanv` has a bit
+    float ks[2][4];                     // by 16 keys: K's scale
     int32_t dead[2][4];                 // nonzero: no page
 };
 
+// Byte of 16-byte piece `piece` (2 * sixteen of keys + lane half) of dim d.
+constexpr int vswap(int d) { return (d & 7) ^ ((d >> 3) & 1); }
 template <int D>
-__device__ __forceinline__ int vword(int d, int piece)
+__device__ __forceinline__ int vbyte(int d, int piece)
 {
-    return 16 * d + 16 * (d / kVB<D>) + 4 * (piece ^ ((d >> 1) & 3));
+    return 128 * (d + d / kVB<D>) + 16 * (piece ^ vswap(d));
 }
 
 // The largest of three (of the others where one is NaN), without the canonicalisation that fmaxf costs.
@@ -775,11 +748,6 @@ __device__ __forceinline__ float max_halves(float x)
 {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return max3(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[1]));
-}
-
-__device__ __forceinline__ i32x8 join8(u32x4 x, u32x4 y)
-{
-    return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
 }
 
 // Sum over the wave, in every lane.
@@ -848,8 +816,7 @@ template <int IO, int D>
 __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_many_kernel(Attend a, int n_chunks, int64_t all_tiles)
 {
     constexpr int QT = IO == kIoF32 ? 3 : 1;                          // 16-bit terms of Q
-    constexpr int N = IO == kIoBF16 ? 2 : 3;                          // terms of P: e4m3, or bf16 for fp32
-    constexpr int PW = IO == kIoF32 ? 4 : 2;                          // 16-byte words of a term of a lane's P
+    constexpr int N = IO == kIoF32 ? 3 : 2;                           // bf16 terms of P
     constexpr int NS = D / 16, NO = D / 32;
     constexpr int KL = D / 16;             // lanes that load a key row
     constexpr int KR = 64 * kManyWaves / KL, KP = 64 / KR;  // key rows of a pass, passes
@@ -929,7 +896,7 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
     // Pages and scales of 16 tiles, a sixteen of keys a lane; those of the next 16 are fetched on the way.
     struct Lanes {
         int64_t at;   // bytes to the page (a key without one, or past the last tile, reads page 0)
-        float ks, ev;
+        float ks, vs;
         int32_t dead;
     };
     auto fetch_pages = [&](int group) {
@@ -939,18 +906,18 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
         return page >= 0 && page < kv.num_blocks ? page : -1;
     };
     auto fetch_scales = [&](int32_t page) {
-        Lanes x{0, 1.0f, 0.0f, 1};
+        Lanes x{0, 1.0f, 1.0f, 1};
         if (page >= 0) {
             x.at = page * kv.c_block;
             x.ks = kv.k_scale[(int64_t)page * kv.nk + kvh];
-            x.ev = (float)scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]);
+            x.vs = pow2(scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]));
             x.dead = 0;
         }
         return x;
     };
-    Lanes here{0, 1.0f, 0.0f, 1};
+    Lanes here{0, 1.0f, 1.0f, 1};
     int32_t page_ahead = -1;
-    auto turn_pages = [&](int i) {  // before load_tile(i), in order
+    auto turn_pages = [&](int i) {  // before load_keys(i), in order
         if (i & 7) return;
         if (i & 8) page_ahead = fetch_pages((i >> 4) + 1);
         else here = fetch_scales(i ? page_ahead : fetch_pages(0));
@@ -959,27 +926,31 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
         const uint32_t lo = __shfl((int)(uint32_t)here.at, l), hi = __shfl((int)(uint32_t)((uint64_t)here.at >> 32), l);
         return (int64_t)(((uint64_t)hi << 32) | lo);
     };
-    float ks_lane = 1.0f, ev_lane = 0.0f;  // of the tile loaded last, where this lane holds one of its sixteens
+    float ks_lane = 1.0f;  // of the keys loaded last, where this lane holds one of the tile's sixteens
     int32_t dead_lane = 1, info = -1;
-    auto load_tile = [&](int i) {
+    const uint8_t *pv = kv.v;  // this thread's rows of the same tile's V, their scale (0: no page)
+    float vs_next = 0.0f, vs = 0.0f;
+    auto load_keys = [&](int i) {
         const int at = (i & 15) * 4;
         const uint8_t *pk[KP];
 #pragma unroll
         for (int p = 0; p < KP; ++p) pk[p] = kv.k + page_at(at + ((kr + p * KR) >> 4)) + koff[p];
-        const uint8_t *pv = kv.v + page_at(at + (vt >> 2)) + voff;
 #pragma unroll
         for (int p = 0; p < KP; ++p) kreg[p] = *reinterpret_cast<const u32x4 *>(pk[p]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vreg[j] = load_vrow<D>(pv + j * kv.c_tok);
+        pv = kv.v + page_at(at + (vt >> 2)) + voff;
+        vs_next = __shfl(here.dead ? 0.0f : here.vs, at + (vt >> 2));
         info = lane - at;
         ks_lane = here.ks;
-        ev_lane = here.ev;
         dead_lane = here.dead;
+    };
+    auto load_values = [&]() {  // of the tile whose keys were loaded last
+        vs = vs_next;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vreg[j] = load_vrow<D>(pv + j * kv.c_tok);
     };
     auto store_info = [&](int i) {
         if ((unsigned)info < 4u) {  // every wave writes the same
             lds.ks[i & 1][info] = ks_lane;
-            lds.ev[i & 1][info] = ev_lane;
             lds.dead[i & 1][info] = dead_lane;
         }
     };
@@ -987,8 +958,7 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
     // others do not, the product goes on without it and the rows are told.
     auto clean_v = [&](int i) {
         const int32_t t0 = c0 + i * 64;
-        if (t0 + 64 <= first && !__any((unsigned)info < 4u && dead_lane)) return;
-        const bool has = !__shfl(here.dead, (i & 15) * 4 + (vt >> 2));
+        if (t0 + 64 <= first && !__any(vs == 0.0f)) return;  // (the lanes' keys are all of the tile's)
         bool nan = false;
 #pragma unroll
         for (int w = 0; w < VB / 4; ++w) {
@@ -997,7 +967,7 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
             for (int j = 0; j < 4; ++j) {
                 uint32_t y = vreg[j].w[w];
                 asm volatile("" : "+v"(y));  // not before the branch
-                if (!has || t0 + 4 * vt + j >= lim_last) y = 0;
+                if (vs == 0.0f || t0 + 4 * vt + j >= lim_last) y = 0;
                 const uint32_t n = (((y & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in a NaN's byte
                 bits |= n << j;
                 vreg[j].w[w] = y & ~(n * 0xffu);
@@ -1005,31 +975,32 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
             *reinterpret_cast<uint32_t *>(&lds.nanv[i & 1][vt][vc * VB + 4 * w]) = bits;
             nan |= bits != 0;
         }
-        if (nan) lds.nan[i & 1] = i + 1;
+        if (nan) lds.nan[i & 1] = i;
     };
-    // keys 4*vt..: tile half vt/8, eight-key group (vt/2)%4, lane half vt%2; the swap of pieces takes four values
-    int vput[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        vput[e] = 16 * VB * vc + 16 * vc + 4 * (((vt & 1) * 2 + (vt >> 3)) ^ ((VB / 2 * vc + e) & 3)) + ((vt >> 1) & 3);
+    // keys 4*vt..: sixteen vt/4, lane half vt%2, first or second half of the piece; dims VB*vc..
+    const int vput = 128 * (VB + 1) * vc + 16 * ((vt >> 2) * 2 + (vt & 1)) + 8 * ((vt >> 1) & 1);
     constexpr int kSlices = KP + VB / 4;
-    auto store_slice = [&](int n, int i, uint32_t *vbuf) {
+    auto store_slice = [&](int n, int i) {  // of tile i's V and tile i + 1's keys
         if (n < KP) {
-            uint8_t *kb = &lds.k[i & 1][kr][2 * kc] + n * KR * (2 * D + 16);
+            uint8_t *kb = &lds.k[(i + 1) & 1][kr][2 * kc] + n * KR * (2 * D + 16);
             const u32x4 x = kreg[n < KP ? n : 0];
             *reinterpret_cast<u32x4 *>(kb) = decode8<IO>(x[0], x[1]);
             *reinterpret_cast<u32x4 *>(kb + 16) = decode8<IO>(x[2], x[3]);
             return;
         }
+        // the bytes of two keys side by side, then bf16 pairs (key, key + 1) of one dim
         const int w = n - KP;
         const uint32_t r0 = vreg[0].w[w], r1 = vreg[1].w[w], r2 = vreg[2].w[w], r3 = vreg[3].w[w];
         const uint32_t a0 = __builtin_amdgcn_perm(r1, r0, 0x05010400u), a1 = __builtin_amdgcn_perm(r3, r2, 0x05010400u);
         const uint32_t b0 = __builtin_amdgcn_perm(r1, r0, 0x07030602u), b1 = __builtin_amdgcn_perm(r3, r2, 0x07030602u);
-        uint32_t *p0 = vbuf + vput[(2 * w) & 3] + 64 * w, *p1 = vbuf + vput[(2 * w + 1) & 3] + 64 * w;
-        p0[0] = __builtin_amdgcn_perm(a1, a0, 0x05040100u);
-        p0[16] = __builtin_amdgcn_perm(a1, a0, 0x07060302u);
-        p1[32] = __builtin_amdgcn_perm(b1, b0, 0x05040100u);
-        p1[48] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+        auto put = [&](int e, uint32_t x, uint32_t y) {
+            const int j = 4 * w + e;  // of the thread's dims
+            *reinterpret_cast<uint2 *>(lds.v[i & 1] + ((vput ^ (16 * (vswap(j) ^ vswap(VB * vc)))) + 128 * j)) = make_uint2(x, y);
+        };
+        put(0, bf16_pair<false>(a0, vs), bf16_pair<false>(a1, vs));
+        put(1, bf16_pair<true>(a0, vs), bf16_pair<true>(a1, vs));
+        put(2, bf16_pair<false>(b0, vs), bf16_pair<false>(b1, vs));
+        put(3, bf16_pair<true>(b0, vs), bf16_pair<true>(b1, vs));
     };
 
     float m = kNoMax, l = 0.0f;
@@ -1042,68 +1013,72 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
     for (int i = 0; i < NO; ++i) pin<IO, D>(o[i]);
 
     // P of the tile before, in terms: its product with V is taken while the next softmax runs
-    u32x4 pf[N][PW];
-    int pexp = 0;
+    u32x4 pf[N][4];
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int e = 0; e < PW; ++e) pf[n][e] = u32x4{0, 0, 0, 0};
-    const int vget0 = vword<D>(col, 2 * half), vget1 = vword<D>(col, 2 * half + 1);
-    auto value_piece = [&](const uint32_t *vbuf, int i, int which) {
-        return *reinterpret_cast<const u32x4 *>(vbuf + (which ? vget1 : vget0) + (512 + 512 / VB) * i);
+        for (int j = 0; j < 4; ++j) pf[n][j] = u32x4{0, 0, 0, 0};
+    // Step u of the product with V: dims 64 * (u / 4).., the sixteen u % 4 of keys; the sums of two pieces of
+    // dims take turns, so neighbouring instructions do not depend on one another.
+    constexpr int kSteps = 2 * NO;
+    int vget[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vget[j] = vbyte<D>(col, 2 * j + half);
+    auto value_piece = [&](int i, int u, int e) {
+        return *reinterpret_cast<const u32x4 *>(lds.v[i & 1] + vget[u & 3] + (4096 + 4096 / VB) * (2 * (u >> 2) + e));
     };
-    auto value_product = [&](int i, u32x4 x0, u32x4 x1) {
-        if constexpr (IO != kIoF32) {
-            const i32x8 vf = join8(x0, x1);
+    auto value_product = [&](int u, u32x4 x0, u32x4 x1) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) o[i] = mfma8(vf, join8(pf[n][0], pf[n][1]), o[i], 127, 119 + pexp - 4 * n);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const u32x4 v = decode8<IO>((h ? x1 : x0)[2 * e], (h ? x1 : x0)[2 * e + 1]);
-#pragma unroll
-                    for (int n = 0; n < N; ++n) o[i] = mfma16<IO>(v, pf[n][2 * h + e], o[i]);
-                }
+        for (int n = 0; n < N; ++n) {
+            o[2 * (u >> 2)] = mfma16<kIoBF16>(x0, pf[n][u & 3], o[2 * (u >> 2)]);
+            o[2 * (u >> 2) + 1] = mfma16<kIoBF16>(x1, pf[n][u & 3], o[2 * (u >> 2) + 1]);
+        }
+    };
+    // The dims in which this lane's row sees a NaN in tile i's V, half of them a lane (rare).
+    auto mark_nan = [&](int i) {
+        if (lds.nan[i & 1] != i) return;
+        const int32_t seen = lim - (c0 + i * 64);
+#pragma unroll 1
+        for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d) {
+            uint32_t bad_d = 0;
+#pragma unroll 1
+            for (int w = 0; w < 16; ++w) bad_d |= lds.nanv[i & 1][w][d] & ((1u << min(max(seen - 4 * w, 0), 4)) - 1);
+            if (bad_d) {
+                lds.bad[r][d >> 5] |= 1u << (d & 31);
+                lds.any_bad = 1;
+            }
         }
     };
 
-    if (tid < 2) lds.nan[tid] = 0;
+    if (tid < 2) lds.nan[tid] = -2;
     if (tid == 2) lds.any_bad = 0;
     for (int i = tid; i < kManyRows * NO; i += 64 * kManyWaves) lds.bad[i / NO][i % NO] = 0;
-    for (int i = tid; i < 16 * (D + 16); i += 64 * kManyWaves) lds.v[2][i] = 0;  // before the first tile: nothing
-    __syncthreads();
+    for (int i = tid; i < 8 * (D + 16); i += 64 * kManyWaves)  // before the first tile: nothing
+        reinterpret_cast<u32x4 *>(lds.v[1])[i] = u32x4{0, 0, 0, 0};
     if (n_tiles > 0) {
         turn_pages(0);
-        load_tile(0);
-        clean_v(0);
+        load_keys(0);
+        load_values();
         store_info(0);
 #pragma unroll
-        for (int n = 0; n < kSlices; ++n) store_slice(n, 0, lds.v[0]);
-        load_tile(1);
+        for (int n = 0; n < KP; ++n) store_slice(n, -1);
+        load_keys(1);
     }
-    // V's buffers of tiles it - 1, it and it + 1
-    uint32_t *vprev = lds.v[2], *vcur = lds.v[0], *vnext = lds.v[1];
-    auto turn = [&]() {
-        uint32_t *x = vprev;
-        vprev = vcur;
-        vcur = vnext;
-        vnext = x;
-    };
     // tiles that this wave's rows see, then those that it only helps to stage
     const int n_mine = min(n_tiles, wlim > c0 ? (wlim - c0 + 63) / 64 : 0);
     int it = 0;
-    for (; it < n_mine; ++it, turn()) {
+    for (; it < n_mine; ++it) {
         const int32_t t0 = c0 + it * 64;
-        __syncthreads();  // tile `it` is in LDS, and tiles it - 1 (K) and it - 2 (V) have been read
-        clean_v(it + 1);
+        // K of tile `it` and V of tile it - 1 are in LDS; K of tile it - 1 and V of tile it - 2 have been read
+        __syncthreads();
+        clean_v(it);
         store_info(it + 1);
         turn_pages(it + 2);
         __builtin_amdgcn_sched_barrier(0);
 
         // The scores, step by step, their operands read kAhead steps before their use; beside them the
-        // next tile goes to LDS, and the one after it is asked for.  (Past the last tile both are done for nobody.)
+        // tile's V and the next tile's K go to LDS, and those after them are asked for.  (Past the last tile
+        // both are done for nobody.)
         constexpr int kAhead = many_resident(IO, D) > 1 ? 2 : 4;
         const uint8_t *kb = &lds.k[it & 1][col][16 * half];
         auto key_piece = [&](int k, int h) { return *reinterpret_cast<const u32x4 *>(kb + h * 32 * (2 * D + 16) + k * 32); };
@@ -1129,25 +1104,26 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
             }
 #pragma unroll
             for (int n = k * kPer; n < (k + 1) * kPer; ++n)
-                if (n < kSlices) store_slice(n, it + 1, vnext);
-            if (k == NS / 2) load_tile(it + 2);
+                if (n < kSlices) store_slice(n, it);
+            if (k == NS / 2) {
+                load_values();
+                load_keys(it + 2);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
-        const bool nan_here = lds.nan[it & 1] == it + 1;
-        float f[4], ev[4];  // by 16 keys: the scores' factor, the exponent of V's scale
+        float f[4];  // by 16 keys: the scores' factor
         int32_t dead[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f[j] = lds.ks[it & 1][j];
-            ev[j] = lds.ev[it & 1][j];
             dead[j] = lds.dead[it & 1][j];
         }
         constexpr int kVAhead = many_resident(IO, D) > 1 ? 1 : 2;
         u32x4 vx[kVAhead + 1][2];  // V's operands
 #pragma unroll
-        for (int i = 0; i < kVAhead && i < NO; ++i) {
-            vx[i][0] = value_piece(vprev, i, 0);
-            vx[i][1] = value_piece(vprev, i, 1);
+        for (int u = 0; u < kVAhead; ++u) {
+            vx[u][0] = value_piece(it - 1, u, 0);
+            vx[u][1] = value_piece(it - 1, u, 1);
         }
 
         // register 4a + b of s[h]: key 32h + 8a + 4*half + b
@@ -1163,9 +1139,8 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
         __builtin_amdgcn_sched_barrier(0);
         // The softmax, and between its steps the tile before's product with V.
         float top[4], m_new = m, ladd = 0.0f;
-        int pexp_new = 0;
         bool moves = false;
-        u32x4 pn[N][PW];
+        u32x4 pn[N][4];
         auto begin = [&]() {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // the largest score of each sixteen
@@ -1178,64 +1153,40 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
             const float m_top = max_halves(max3(max3(top[0], top[1], top[2]), top[3], m));
             moves = __any(m_top > m + 8.0f);
             m_new = moves ? m_top : m;
-            if constexpr (IO != kIoF32) {
-                const float big = max3(max3(top[0] + ev[0], top[1] + ev[1], top[2] + ev[2]), top[3] + ev[3], -1e30f);
-                pexp_new = (int)fminf(fmaxf(__builtin_ceilf(max_halves(big) - m_new), -90.0f), 121.0f);
-            }
         };
-        float sum4[8];
-        auto four = [&](int n) {  // p of registers 4*(n%4).. of s[n/4]: four keys of sixteen n/2
-            const int j = n >> 1;
-            float p[4];
-            if constexpr (IO != kIoF32) {
-                const float up = ev[j] - (float)(pexp_new - 8), add = up - m_new;
+        auto two = [&](int n) {  // p of registers 2*(n%8).. of s[n/8]: two keys of sixteen n/4
+            float p[2];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n >> 2][4 * (n & 3) + q], f[j], add));
-                sum4[n] = (p[0] + p[1]) + (p[2] + p[3]);
-                if (n & 1) ladd += __builtin_ldexpf(sum4[n - 1] + sum4[n], -(int)up);
-                uint32_t w[N];
-                split4<N>(p[0], p[1], p[2], p[3], w);
+            for (int q = 0; q < 2; ++q) p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n >> 3][2 * (n & 7) + q], f[n >> 2], -m_new));
+            ladd += p[0] + p[1];
 #pragma unroll
-                for (int t = 0; t < N; ++t) pn[t][n >> 2][n & 3] = w[t];
-            } else {
-                const float vs = pow2((int)ev[j]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n >> 2][4 * (n & 3) + q], f[j], -m_new));
-                    ladd += p[q];
-                    p[q] *= vs;
-                }
-#pragma unroll
-                for (int t = 0; t < N; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t w = pack16x2<kIoBF16>(p[2 * e], p[2 * e + 1]);
-                        float lo, hi;
-                        unpack16x2<kIoBF16>(w, lo, hi);
-                        p[2 * e] -= lo;
-                        p[2 * e + 1] -= hi;
-                        pn[t][j][2 * (n & 1) + e] = w;
-                    }
+            for (int t = 0; t < N; ++t) {
+                const uint32_t w = pack16x2<kIoBF16>(p[0], p[1]);
+                float lo, hi;
+                unpack16x2<kIoBF16>(w, lo, hi);
+                p[0] -= lo;
+                p[1] -= hi;
+                pn[t][n >> 2][n & 3] = w;
             }
         };
 #pragma unroll
-        for (int i = 0; i < NO; ++i) {
-            if (i + kVAhead < NO) {
-                vx[(i + kVAhead) % (kVAhead + 1)][0] = value_piece(vprev, i + kVAhead, 0);
-                vx[(i + kVAhead) % (kVAhead + 1)][1] = value_piece(vprev, i + kVAhead, 1);
+        for (int u = 0; u < kSteps; ++u) {
+            if (u + kVAhead < kSteps) {
+                vx[(u + kVAhead) % (kVAhead + 1)][0] = value_piece(it - 1, u + kVAhead, 0);
+                vx[(u + kVAhead) % (kVAhead + 1)][1] = value_piece(it - 1, u + kVAhead, 1);
             }
-            value_product(i, vx[i % (kVAhead + 1)][0], vx[i % (kVAhead + 1)][1]);
-            if (i == 0) begin();
+            value_product(u, vx[u % (kVAhead + 1)][0], vx[u % (kVAhead + 1)][1]);
+            if (u == 0) begin();
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
-                if (i > 0 && n * (NO - 1) / 8 == i - 1) four(n);
+            for (int n = 0; n < 16; ++n)
+                if (u > 0 && n * (kSteps - 1) / 16 == u - 1) two(n);
             __builtin_amdgcn_sched_barrier(0);
         }
         // (P is finished here and not beyond the branch below, where nothing runs beside it)
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int e = 0; e < PW; ++e) asm volatile("" : "+v"(pn[n][e]));
+            for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(pn[n][j]));
         asm volatile("" : "+v"(ladd));
         __builtin_amdgcn_sched_barrier(0);
         if (moves) {
@@ -1250,38 +1201,30 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
             m = m_new;
         }
         l += ladd;
-        pexp = pexp_new;
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int e = 0; e < PW; ++e) pf[n][e] = pn[n][e];
+            for (int j = 0; j < 4; ++j) pf[n][j] = pn[n][j];
 #pragma unroll
         for (int i = 0; i < NO; ++i) pin<IO, D>(o[i]);
-        if (nan_here) {  // rare: the dims in which this lane's row sees a NaN, half of them a lane
-            const int32_t seen = lim - t0;
-#pragma unroll 1
-            for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d) {
-                uint32_t bad_d = 0;
-#pragma unroll 1
-                for (int w = 0; w < 16; ++w) bad_d |= lds.nanv[it & 1][w][d] & ((1u << min(max(seen - 4 * w, 0), 4)) - 1);
-                if (bad_d) {
-                    lds.bad[r][d >> 5] |= 1u << (d & 31);
-                    lds.any_bad = 1;
-                }
-            }
-        }
+        mark_nan(it - 1);
     }
-    // (its buffer is written again two barriers from here)
-#pragma unroll
-    for (int i = 0; i < NO; ++i) value_product(i, value_piece(vprev, i, 0), value_piece(vprev, i, 1));
-    for (; it < n_tiles; ++it, turn()) {
+    for (const int last = it; it <= n_tiles; ++it) {
         __syncthreads();
-        clean_v(it + 1);
-        store_info(it + 1);
-        turn_pages(it + 2);
+        if (it < n_tiles) {
+            clean_v(it);
+            store_info(it + 1);
+            turn_pages(it + 2);
 #pragma unroll
-        for (int n = 0; n < kSlices; ++n) store_slice(n, it + 1, vnext);
-        load_tile(it + 2);
+            for (int n = 0; n < kSlices; ++n) store_slice(n, it);
+            load_values();
+            load_keys(it + 2);
+        }
+        if (it == last) {
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) value_product(u, value_piece(it - 1, u, 0), value_piece(it - 1, u, 1));
+            mark_nan(it - 1);
+        }
     }
 
     l += __shfl_xor(l, 32);

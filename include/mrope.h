@@ -397,9 +397,8 @@ mrope_status mrope_decode_kv8(void *q, int64_t q_tok_stride, int64_t q_head_stri
  * lse        nullable, [n_tokens][n_q_heads] fp32: ln sum_j exp(score_j); -infinity for a row that
  *            sees nothing.
  * Precision: scores and sums in fp32; queries are not rounded (16-bit types) or kept to 2^-24
- *            (fp32).  Probabilities are kept to 2^-24 of their size for fp32; for the 16-bit types to 2^-16
- *            where the sequences bring few query rows (on the average up to 32 for a KV head), else to
- *            2^-8 (bf16) or 2^-12 (fp16), but not below 2^-22 of the largest (times V's scale) of 64 positions.
+ *            (fp32).  Probabilities are kept to 2^-16 of their size for the 16-bit types and to 2^-24 for
+ *            fp32, whatever else the call holds.
  *            What a row does not see reaches it in no way, NaN codes among it.
  * workspace  256-byte aligned device memory of mrope_attend_kv8_workspace_bytes(...) bytes (0: may be
  *            NULL), needing no initialisation; calls that share one must be ordered.
