@@ -38,7 +38,7 @@ __device__ __forceinline__ bool make_tile(const Attend &a, int g, int32_t s, int
     t.s = s;
     t.t0 = t0;
     t.rows = len * g;
-    if (k * R >= t.rows) return false;
+    if (k < 0 || k * R >= t.rows) return false;
     t.row0 = (int32_t)k * R;
     const int64_t ctx = max(a.ctx[s], 0);
     t.past = ctx - len;
@@ -778,14 +778,14 @@ __device__ __forceinline__ bool find_long_tile(const Attend &a, int g, int64_t r
     const int32_t t0 = !in ? 0 : (a.cu ? a.cu[lane] : lane);
     const int32_t len = !in ? 0 : (a.cu ? (int32_t)max(min((int64_t)a.cu[lane + 1], a.n_tokens) - t0, (int64_t)0) : 1);
     const int32_t tiles = (int32_t)(((int64_t)len * g + R - 1) / R);
-    const int32_t past = in ? max(a.ctx[lane], 0) - len : 0;
+    const int32_t past = seen_of(a, lane, in) - len;  // (at most 2^27: a length past the table ranks as the table)
     if (rank >= wave_sum(tiles)) return false;
     auto count = [&](int64_t x) {  // of the lane's tiles that are ranked by x or more: k + 1 >= (x - past) g / R
         const int64_t k1 = ((x - past) * g + R - 1) >> __builtin_ctz(R);
         return tiles - (int32_t)min(max(k1 - 1, (int64_t)0), (int64_t)tiles);
     };
     int32_t lo32 = tiles ? past : 0x7fffffff;
-    int32_t span = 0;  // of the ranks, from the least past on
+    int32_t span = 0;  // of the ranks, from the least past on (below 2^28: the rows of a call are below 2^26)
 #pragma unroll
     for (int x = 1; x < 64; x *= 2) lo32 = min(lo32, __shfl_xor(lo32, x));
     if (tiles) span = (int32_t)min((int64_t)past - lo32 + (int64_t)R * tiles / g + 1, (int64_t)0x7fffffff);

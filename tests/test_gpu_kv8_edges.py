@@ -1,0 +1,56 @@
+"""The 8-bit cache's calls at the edges of what their documentation allows."""
+import math
+
+import pytest
+import torch
+
+import canvas_rope_rotary_amd as mr
+import kv8_ref as ref
+from gpu_util import say
+from test_gpu_kv8 import F8, HALF_STEP, World, check_append, i32, same_codes
+
+pytestmark = pytest.mark.gpu
+KEPT = {"bf16": 2.0 ** -16, "f16": 2.0 ** -16, "f32": 2.0 ** -24}
+I32 = 2 ** 31 - 1
+
+
+def check(w, cu, ctx, q, dtype, n, *, softmax_scale=None, out=None, cache=None, extra=0.0, what=""):
+    """attend_kv8 on World w against 64 bits: tolerances of the documented precision (a score: at most three
+    exact terms a product, each sum rounded; l and the output: n positions of at most three terms; exp2 an
+    ulp; `extra` of the spread where a test's numbers need it).  Rows behind cu's last are left alone."""
+    T, D = (q.shape[0] if cu is None else cu[-1]), q.shape[2]
+    o_dev = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda") if out is None else out
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    mr.attend_kv8(q.cuda(), None if cu is None else i32(cu).cuda(), i32(ctx).cuda(), w.tables.cuda(), *(cache or w.cache()),
+                  softmax_scale=softmax_scale, out=o_dev, lse=lse)
+    o, z, spread, amp = ref.attend(q[:T], cu, ctx, w.tables.tolist(), w.kc, w.vc, w.ks, w.vs, softmax_scale)
+    got, gz = o_dev[:T].cpu().double(), lse[:T].cpu().double()
+    ds = ((3 * D + 8) * 2.0 ** -24 + (2.0 ** -24 if dtype == "f32" else 0)) * amp
+    tol = HALF_STEP[dtype] * o.abs() * 1.01 + (2 * ds[..., None] + KEPT[dtype] + 2.0 ** -22 + (4 * n + 4) * 2.0 ** -24 + extra) * spread
+    tol += 2.0 ** -24 if dtype == "f16" else 2.0 ** -120
+    bad = ~((got - o).abs() <= tol)
+    assert not bool(bad.any()), (what, int(bad.sum()), bad.nonzero()[:4].tolist(), got[bad][:4].tolist(), o[bad][:4].tolist())
+    fin = torch.isfinite(z)
+    assert torch.equal(fin, torch.isfinite(gz)), what
+    dz = (gz[fin] - z[fin]).abs()
+    assert bool((dz <= ds[fin] + (n + 4) * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -22 * z[fin].abs()).all()), (what, float(dz.max()))
+    assert bool((got[~fin] == 0).all()), what
+    assert bool((o_dev[T:] == 7.0).all()) and bool((lse[T:] == 7.0).all()), what
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n_seqs", [5, 70])
+def test_lengths_past_the_table(dtype, n_seqs):
+    """Lengths at the top of int32 (every position of the table is seen), next to none and negative ones,
+    for prompts (ranked by length up to 64 sequences) and for single tokens."""
+    say("past the table", dtype, n_seqs)
+    w = World([96] * n_seqs, 16, 2, 64, seed=n_seqs)
+    lens = ([40, 150, 0, 1, 77] * 14)[:n_seqs]
+    ctx = ([I32, 0, 5, I32 - 1, 90] * 14)[:n_seqs]
+    ctx[-1] = -I32 - 1
+    cu = [0]
+    for m in lens:
+        cu.append(cu[-1] + m)
+    check(w, cu, ctx, w.heads(cu[-1] + 3, 6, dtype), dtype, 96, what="prompts")
+    check(w, None, ctx, w.heads(n_seqs, 6, dtype), dtype, 96, what="tokens")
+    check(w, list(range(n_seqs + 1)), ctx, w.heads(n_seqs + 2, 6, dtype), dtype, 96, what="tokens by cu")
