@@ -21,6 +21,14 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kNoMax = -3.0e38f;  // the running maximum before any visible key
 
+// V is decoded 2^8 smaller than it is and the output divided by l / 2^8: a code times its scale can pass
+// fp32's largest value (448 * 2^120), and the sums have as much room above it; the smallest, 2^-9 * 2^-96, stays far above
+// the smallest normal bf16.
+constexpr int kVDown = 8;
+constexpr float kVUp = 256.0f;
+
+__device__ __forceinline__ float out_factor(float l) { return l == 0.0f ? 0.0f : kVUp / l; }
+
 // ------------------------------------------------------------------ the work of a workgroup ----
 struct Tile {
     int32_t s;          // sequence
@@ -382,7 +390,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_ke
             valid = page >= 0 && page < kv.num_blocks;
             if (valid) {
                 ks = kv.k_scale[(int64_t)page * kv.nk + kvh];
-                vs = kv.v_scale[(int64_t)page * kv.nk + kvh];
+                vs = kv.v_scale[(int64_t)page * kv.nk + kvh] * (1.0f / kVUp);
                 base = page * kv.c_block;
             }
             base += (tok & (kv.block_size - 1)) * kv.c_tok + kvh * kv.c_head;
@@ -615,7 +623,7 @@ __global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_ke
             const int rw = tl.row0 + rr;
             const int64_t tok = tl.t0 + rw / g;
             const int head = kvh * g + rw % g;
-            const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
+            const float inv = out_factor(ll);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = ll == 0.0f ? 0.0f : y[i] * inv;
             store_out8<IO>(a, tok * a.o_tok + head * a.o_head + d, y);
@@ -715,6 +723,11 @@ __device__ __forceinline__ u32x4 decode8(uint32_t u, uint32_t v)
 template <int D>
 constexpr int kVB = D / 16;  // dims of V a thread transposes, for four keys
 
+// A sixteen of keys: it has no page; its values may pass 2^90, so P must not exceed 1 beside them (2^8 * 2^90 and
+// 2^27 positions still sum below fp32's largest).
+constexpr int32_t kNoPage = 1, kLarge = 2;
+constexpr int kLargeExp = 80;
+
 template <int D>
 struct alignas(16) ManyLds {
     uint8_t k[2][64][2 * D + 16];       // 16-bit keys
@@ -724,7 +737,7 @@ struct alignas(16) ManyLds {
     int32_t any_bad;
     int32_t nan[2];                     // the last tile in which `nanv` has a bit
     float ks[2][4];                     // by 16 keys: K's scale
-    int32_t dead[2][4];                 // nonzero: no page
+    int32_t flags[2][4];                // kNoPage, kLarge
 };
 
 // Byte of 16-byte piece `piece` (2 * sixteen of keys + lane half) of dim d.
@@ -897,7 +910,7 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
     struct Lanes {
         int64_t at;   // bytes to the page (a key without one, or past the last tile, reads page 0)
         float ks, vs;
-        int32_t dead;
+        int32_t flags;
     };
     auto fetch_pages = [&](int group) {
         const int32_t tok = c0 + (group * 64 + lane) * 16;
@@ -906,16 +919,17 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
         return page >= 0 && page < kv.num_blocks ? page : -1;
     };
     auto fetch_scales = [&](int32_t page) {
-        Lanes x{0, 1.0f, 1.0f, 1};
+        Lanes x{0, 1.0f, 1.0f, kNoPage};
         if (page >= 0) {
             x.at = page * kv.c_block;
             x.ks = kv.k_scale[(int64_t)page * kv.nk + kvh];
-            x.vs = pow2(scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]));
-            x.dead = 0;
+            const int e = scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]);
+            x.vs = pow2(e - kVDown);
+            x.flags = e > kLargeExp ? kLarge : 0;
         }
         return x;
     };
-    Lanes here{0, 1.0f, 1.0f, 1};
+    Lanes here{0, 1.0f, 1.0f, kNoPage};
     int32_t page_ahead = -1;
     auto turn_pages = [&](int i) {  // before load_keys(i), in order
         if (i & 7) return;
@@ -927,7 +941,7 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
         return (int64_t)(((uint64_t)hi << 32) | lo);
     };
     float ks_lane = 1.0f;  // of the keys loaded last, where this lane holds one of the tile's sixteens
-    int32_t dead_lane = 1, info = -1;
+    int32_t flags_lane = kNoPage, info = -1;
     const uint8_t *pv = kv.v;  // this thread's rows of the same tile's V, their scale (0: no page)
     float vs_next = 0.0f, vs = 0.0f;
     auto load_keys = [&](int i) {
@@ -938,10 +952,10 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
 #pragma unroll
         for (int p = 0; p < KP; ++p) kreg[p] = *reinterpret_cast<const u32x4 *>(pk[p]);
         pv = kv.v + page_at(at + (vt >> 2)) + voff;
-        vs_next = __shfl(here.dead ? 0.0f : here.vs, at + (vt >> 2));
+        vs_next = __shfl(here.flags & kNoPage ? 0.0f : here.vs, at + (vt >> 2));
         info = lane - at;
         ks_lane = here.ks;
-        dead_lane = here.dead;
+        flags_lane = here.flags;
     };
     auto load_values = [&]() {  // of the tile whose keys were loaded last
         vs = vs_next;
@@ -951,7 +965,7 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
     auto store_info = [&](int i) {
         if ((unsigned)info < 4u) {  // every wave writes the same
             lds.ks[i & 1][info] = ks_lane;
-            lds.dead[i & 1][info] = dead_lane;
+            lds.flags[i & 1][info] = flags_lane;
         }
     };
     // What no row sees may hold anything: it must not reach the product; and where some rows see a NaN and
@@ -1112,11 +1126,11 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
             __builtin_amdgcn_sched_barrier(0);
         }
         float f[4];  // by 16 keys: the scores' factor
-        int32_t dead[4];
+        int32_t flags[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f[j] = lds.ks[it & 1][j];
-            dead[j] = lds.dead[it & 1][j];
+            flags[j] = lds.flags[it & 1][j];
         }
         constexpr int kVAhead = many_resident(IO, D) > 1 ? 1 : 2;
         u32x4 vx[kVAhead + 1][2];  // V's operands
@@ -1127,13 +1141,13 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
         }
 
         // register 4a + b of s[h]: key 32h + 8a + 4*half + b
-        if (t0 + 64 > wfirst || __any(dead[0] | dead[1] | dead[2] | dead[3])) {
+        if (t0 + 64 > wfirst || __any((flags[0] | flags[1] | flags[2] | flags[3]) & kNoPage)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int key = 32 * h + 8 * (q >> 2) + 4 * half + (q & 3);
-                    if (t0 + key >= lim || dead[2 * h + (q >> 3)]) s[h][q] = -__builtin_inff();
+                    if (t0 + key >= lim || (flags[2 * h + (q >> 3)] & kNoPage)) s[h][q] = -__builtin_inff();
                 }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -1149,9 +1163,11 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
                 top[j] = max3(max3(max3(s[h][q], s[h][q + 1], s[h][q + 2]), s[h][q + 3], s[h][q + 4]), s[h][q + 5], s[h][q + 6]);
                 top[j] = max3(top[j], s[h][q + 7], s[h][q + 7]) * f[j];
             }
-            // the maximum moves only where it has grown by 2^8: until then p exceeds 1 and nothing is lost
+            // the maximum moves only where it has grown by 2^8: until then p exceeds 1 and nothing is lost (but
+            // beside large values, where the sums have no room for it, it moves at once)
             const float m_top = max_halves(max3(max3(top[0], top[1], top[2]), top[3], m));
-            moves = __any(m_top > m + 8.0f);
+            const bool large = (flags[0] | flags[1] | flags[2] | flags[3]) & kLarge;
+            moves = __any(m_top > m + (large ? 0.0f : 8.0f));
             m_new = moves ? m_top : m;
         };
         auto two = [&](int n) {  // p of registers 2*(n%8).. of s[n/8]: two keys of sixteen n/4
@@ -1241,7 +1257,7 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
     const int64_t tok = tl.t0 + row / g;
     const int head = kvh * g + row % g;
     if (lim_last <= chunk) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // (a row that saw nothing has summed nothing)
+        const float inv = out_factor(l);  // (a row that saw nothing has summed nothing)
 #pragma unroll
         for (int i = 0; i < NO; ++i)
 #pragma unroll
@@ -1358,7 +1374,7 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(Attend a, int
     const int rw = tl.row0 + rr;
     const int64_t tok = tl.t0 + rw / g;
     const int head = kvh * g + rw % g;
-    const float inv = 1.0f / ll;
+    const float inv = out_factor(ll);
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = ll == 0.0f ? 0.0f : r[i] * inv;
     store_out8<IO>(a, tok * a.o_tok + head * a.o_head + 8 * e, r);

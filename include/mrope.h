@@ -398,7 +398,8 @@ mrope_status mrope_decode_kv8(void *q, int64_t q_tok_stride, int64_t q_head_stri
  *            sees nothing.
  * Precision: scores and sums in fp32; queries are not rounded (16-bit types) or kept to 2^-24
  *            (fp32).  Probabilities are kept to 2^-16 of their size for the 16-bit types and to 2^-24 for
- *            fp32, whatever else the call holds.
+ *            fp32, whatever else the call holds.  The sum over p_j v_j is held 2^8 smaller, p_j as parts of the
+ *            largest: that has to stay below fp32's largest value.
  *            What a row does not see reaches it in no way, NaN codes among it.
  * workspace  256-byte aligned device memory of mrope_attend_kv8_workspace_bytes(...) bytes (0: may be
  *            NULL), needing no initialisation; calls that share one must be ordered.

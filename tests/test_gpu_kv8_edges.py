@@ -54,3 +54,63 @@ def test_lengths_past_the_table(dtype, n_seqs):
     check(w, cu, ctx, w.heads(cu[-1] + 3, 6, dtype), dtype, 96, what="prompts")
     check(w, None, ctx, w.heads(n_seqs, 6, dtype), dtype, 96, what="tokens")
     check(w, list(range(n_seqs + 1)), ctx, w.heads(n_seqs + 2, 6, dtype), dtype, 96, what="tokens by cu")
+
+
+def prompts_and_tokens(w, n, hq, dtype, what, q=None, lens=(90, 60), softmax_scale=None, extra=0.0):
+    """The World's first two sequences of n positions as pieces of prompts and as single tokens."""
+    cu = [0, lens[0], sum(lens)]
+    q = w.heads(cu[-1], hq, dtype) if q is None else q
+    check(w, cu, [n] * 2, q, dtype, n, softmax_scale=softmax_scale, extra=extra, what=(what, "prompts"))
+    check(w, None, [n] * 2, q[[7, cu[-1] - 1]], dtype, n, softmax_scale=softmax_scale, extra=extra, what=(what, "tokens"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [256, 64])
+def test_value_scales_side_by_side(dtype, D):
+    """Pages of V whose scales differ by up to 2^216: zero pages (as an append leaves them) next to large ones,
+    and both ends of the range; scores that rise along the context, so that the running maximum follows."""
+    say("value scales", dtype, D)
+    for case, exps in enumerate(((-96, 0, 30), (-96, 60), (-96, -96, 118), (-96, -90), (-9, -5, 25), (118, 110, 80))):
+        w = World([200, 200], 16, 2, D, seed=case)
+        pick = torch.randint(0, len(exps), w.vs.shape, generator=w.g)
+        w.vs = torch.exp2(torch.tensor(exps)[pick].float())
+        zero = (w.vs == 2.0 ** -96) & (len(set(exps)) > 1)
+        w.vc.view(torch.uint8)[zero[:, None, :, None].expand_as(w.vc)] = 0
+        w.vc = w.vc.float().clamp(-255, 255).to(F8)  # (at 2^118 to 2^126)
+        prompts_and_tokens(w, 200, 4, dtype, exps)
+        q = w.heads(150, 4, dtype, 3.0)
+        prompts_and_tokens(w, 200, 4, dtype, (exps, "wide scores"), q)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_largest_values(dtype):
+    """Codes of 448 at a scale of 2^120 (past fp32's largest): rows that do not see them are untouched, and a
+    row's average of them is right where it can be held."""
+    say("largest values", dtype)
+    w = World([100, 100], 16, 2, 128, seed=31)
+    for s in range(2):
+        page = int(w.tables[s, 5])
+        w.vs[page, 1] = 2.0 ** 120
+        w.vc.view(torch.uint8)[page, :, 1] = 0x7e
+    q = w.heads(150, 4, dtype)
+    for cu, qq in (([0, 90, 150], q), (None, q[:2])):
+        ctx = [100, 84 + 4]
+        out, _ = mr.attend_kv8(qq.cuda(), None if cu is None else i32(cu).cuda(), i32(ctx).cuda(), w.tables.cuda(), *w.cache())
+        o, z, spread, amp = ref.attend(qq, cu, ctx, w.tables.tolist(), w.kc, w.vc, w.ks, w.vs)
+        held = o.abs() < 2.0 ** 127
+        assert bool(held.any()) and bool((o.abs() > 2.0 ** 100).any())
+        ds = (3 * 128 + 9) * 2.0 ** -24 * amp[..., None]
+        tol = HALF_STEP[dtype] * o.abs() * 1.01 + (2 * ds + KEPT[dtype] + 2.0 ** -22 + 404 * 2.0 ** -24) * spread
+        got = out.cpu().double()
+        assert bool(((got - o).abs() <= tol)[held].all()), (cu, float(((got - o).abs() / tol)[held].max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_key_scales(dtype):
+    """Pages of K at both ends of the scales' range, under queries that bring the scores back."""
+    say("key scales", dtype)
+    for case, e in enumerate((-90, -40, 60, 100)):
+        w = World([200, 200], 16, 2, 128, seed=40 + case)
+        w.ks = w.ks * 2.0 ** e
+        w.ks[::3] = 2.0 ** max(e - 30, -96)
+        prompts_and_tokens(w, 200, 4, dtype, e, w.heads(150, 4, dtype) * 2.0 ** -e)
