@@ -1159,7 +1159,7 @@ __global__ __launch_bounds__(64 * kManyWaves, many_resident(IO, D)) void attend_
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // the largest score of each sixteen
                 const int h = j >> 1, q = 8 * (j & 1);
-                f[j] *= factor;
+                f[j] = fmaxf(f[j] * factor, 0x1p-126f);  // not 0, which would make a masked -infinity NaN
                 top[j] = max3(max3(max3(s[h][q], s[h][q + 1], s[h][q + 2]), s[h][q + 3], s[h][q + 4]), s[h][q + 5], s[h][q + 6]);
                 top[j] = max3(top[j], s[h][q + 7], s[h][q + 7]) * f[j];
             }

@@ -114,3 +114,18 @@ def test_key_scales(dtype):
         w.ks = w.ks * 2.0 ** e
         w.ks[::3] = 2.0 ** max(e - 30, -96)
         prompts_and_tokens(w, 200, 4, dtype, e, w.heads(150, 4, dtype) * 2.0 ** -e)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("softmax_scale", [1e-18, -1e-20, 1e-30, 1e-44])
+def test_tiny_factors(dtype, softmax_scale):
+    """Factors so small that with a small page scale they vanish: every position that a row sees weighs the
+    same, and those that it does not see weigh nothing."""
+    say("tiny factor", dtype, softmax_scale)
+    w = World([200, 200], 16, 2, 128, seed=50)
+    w.ks.fill_(2.0 ** -96)
+    w.kc.view(torch.uint8)[:] = 0
+    prompts_and_tokens(w, 200, 4, dtype, "zero keys", softmax_scale=softmax_scale)
+    w.ks[1::2] = 2.0 ** -20
+    w.kc = (torch.randn(w.kc.shape, generator=w.g) * 100).to(F8)
+    prompts_and_tokens(w, 200, 4, dtype, "small keys", softmax_scale=softmax_scale)
