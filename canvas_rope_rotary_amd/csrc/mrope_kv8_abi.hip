@@ -1,6 +1,7 @@
 // C ABI of the 8-bit paged K/V cache: argument checks and launches of the append, the attention and
 // the page calls.  The entry points are declared and documented in include/mrope.h.
 #include <cmath>
+#include <numeric>
 
 #include "mrope_kv8.h"
 #include "mrope_pages.h"
@@ -41,6 +42,28 @@ mrope_status check_kv8(const void *k_cache, const void *v_cache, const float *k_
     if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(tables, 4))
         return fail(MROPE_ERR_ALIGN, "scales and block_tables must be 4-byte aligned");
     return MROPE_OK;
+}
+
+// Heads of two buffers (n_tokens x n_heads rows of head_dim elements each, element strides) that share bytes:
+// views of one buffer may interleave.  Exact for one token stride; for two, tokens count as lying anywhere that
+// the strides' common divisor allows.
+bool heads_overlap(const void *a, int64_t a_tok, int64_t a_head, const void *b, int64_t b_tok, int64_t b_head, int32_t n_heads,
+                   int64_t n_tokens, int32_t head_dim, int64_t elem_bytes)
+{
+    const int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / elem_bytes;  // (16-byte aligned both)
+    const int64_t a_span = (n_tokens - 1) * a_tok + (n_heads - 1) * a_head + head_dim;
+    const int64_t b_span = (n_tokens - 1) * b_tok + (n_heads - 1) * b_head + head_dim;
+    if (d >= a_span || -d >= b_span) return false;
+    const int64_t tok = n_tokens > 1 ? std::gcd(a_tok, b_tok) : 0;
+    const int64_t most = n_tokens > 1 && a_tok != b_tok ? INT64_MAX : n_tokens - 1;
+    for (int32_t i = 0; i < n_heads; ++i)
+        for (int32_t j = 0; j < n_heads; ++j) {
+            // rows t tokens apart meet if t * tok is less than head_dim from x
+            const int64_t x = d + j * b_head - i * a_head, near = tok > 0 ? x / tok : 0;
+            for (int64_t t = near - 1; t <= near + 1; ++t)
+                if (t >= -most && t <= most && t * tok - x < head_dim && x - t * tok < head_dim) return true;
+        }
+    return false;
 }
 
 Kv8 make_kv8(const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale, int64_t num_blocks,
@@ -276,7 +299,9 @@ mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_hea
         if (!aligned(workspace, 256)) return fail(MROPE_ERR_WORKSPACE, "workspace not 256-byte aligned");
         if (workspace_bytes < need) return fail(MROPE_ERR_WORKSPACE, "workspace too small (%zu < %zu)", workspace_bytes, need);
     }
-    if (out == q) return fail(MROPE_ERR_ARG, "out must not be q");
+    if (heads_overlap(q, q_tok_stride, q_head_stride, out, out_tok_stride, out_head_stride, n_q_heads, n_tokens, head_dim,
+                      dtype == MROPE_F32 ? 4 : 2))
+        return fail(MROPE_ERR_ARG, "out must not overlap q");
     Attend a{};
     a.q = q;
     a.out = out;

@@ -392,8 +392,8 @@ mrope_status mrope_decode_kv8(void *q, int64_t q_tok_stride, int64_t q_head_stri
  *            (they are the last ones).  Query token i of len sees the positions j <= context - len + i
  *            that its table holds.
  * softmax_scale  the scores' factor (1/sqrt(head_dim) as a rule).
- * out        [n_tokens] heads of `dtype` (may not overlap q): sum_j p_j v_j / sum_j p_j.  A row that
- *            sees nothing is 0.
+ * out        [n_tokens] heads of `dtype`: sum_j p_j v_j / sum_j p_j.  A row that sees nothing is 0.  May
+ *            not overlap q (refused); both may be views of one buffer, other heads or other tokens of it.
  * lse        nullable, [n_tokens][n_q_heads] fp32: ln sum_j exp(score_j); -infinity for a row that
  *            sees nothing.
  * Precision: scores and sums in fp32; queries are not rounded (16-bit types) or kept to 2^-24

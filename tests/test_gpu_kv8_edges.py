@@ -129,3 +129,31 @@ def test_tiny_factors(dtype, softmax_scale):
     w.ks[1::2] = 2.0 ** -20
     w.kc = (torch.randn(w.kc.shape, generator=w.g) * 100).to(F8)
     prompts_and_tokens(w, 200, 4, dtype, "small keys", softmax_scale=softmax_scale)
+
+
+def test_output_and_queries_of_one_buffer():
+    """Views of one buffer that share no row are taken, those that do are refused and nothing is written."""
+    say("one buffer")
+    w = World([150, 40], 16, 2, 64, seed=60)
+    cu, ctx = [0, 70, 90], [150, 40]
+    for what, q_at, o_at in (("heads of a token", (slice(None, 90), slice(0, 4)), (slice(None, 90), slice(4, 8))),
+                             ("tokens", (slice(0, 90), slice(0, 4)), (slice(90, 180), slice(2, 6))),
+                             ("turns", (slice(0, 180, 2), slice(0, 4)), (slice(1, 180, 2), slice(1, 5))),
+                             ("strides", (slice(0, 180, 2), slice(0, 4)), (slice(0, 90), slice(4, 8)))):
+        big = w.heads(180, 8, "bf16").cuda()
+        q, out = big[q_at], big[o_at]
+        out.fill_(7.0)
+        check(w, cu, ctx, q.clone().cpu(), "bf16", 150)
+        want = mr.attend_kv8(q.clone(), i32(cu).cuda(), i32(ctx).cuda(), w.tables.cuda(), *w.cache())[0]
+        kept = big.clone()
+        mr.attend_kv8(q, i32(cu).cuda(), i32(ctx).cuda(), w.tables.cuda(), *w.cache(), out=out)
+        assert torch.equal(out, want), what
+        kept[o_at] = want
+        assert torch.equal(big, kept), what
+    for q_at, o_at in (((slice(0, 90), slice(0, 4)), (slice(0, 90), slice(3, 7))), ((slice(0, 90), slice(0, 4)), (slice(1, 91), slice(0, 4))),
+                       ((slice(0, 180, 2), slice(0, 4)), (slice(0, 90), slice(3, 7)))):
+        big = w.heads(180, 8, "bf16").cuda()
+        kept = big.clone()
+        with pytest.raises(mr.MropeError, match="overlap"):
+            mr.attend_kv8(big[q_at], i32(cu).cuda(), i32(ctx).cuda(), w.tables.cuda(), *w.cache(), out=big[o_at])
+        assert torch.equal(big, kept)
