@@ -21,23 +21,24 @@ constexpr int kPlan = 1024;  // threads of the plan kernels
 constexpr int32_t kNotEnough = 1, kBadRow = 2;  // MROPE_PAGES_*
 
 // Exclusive prefix sum of v over the workgroup; total in `sum`.
-__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t &sum)
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T &sum)
 {
-    __shared__ int32_t part[kPlan / 64];
+    __shared__ T part[kPlan / 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int32_t x = v;
+    T x = v;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int32_t y = __shfl_up(x, o);
+        const T y = __shfl_up(x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();  // `part` of an earlier scan has been read
     if (lane == 63) part[wave] = x;
     __syncthreads();
-    int32_t before = 0, all = 0;
+    T before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kPlan / 64; ++w) {
-        const int32_t p = part[w];
+        const T p = part[w];
         if (w < wave) before += p;
         all += p;
     }
@@ -104,11 +105,11 @@ __device__ void claim_rows(const int32_t *rows, int32_t n, int32_t n_rows, int32
 template <typename Need>
 __device__ void plan_requests(const Pages &p, int32_t n, const PagesWs &ws, int32_t *status, Need need)
 {
-    int64_t wanted = 0;
+    int64_t wanted = 0, sum;  // (a table's width of pages for each request may pass 32 bits together)
     for (int32_t b = 0; b < n; b += kPlan) {
         const int32_t i = b + threadIdx.x;
-        int32_t want = i < n ? need(i) : 0, sum;
-        const int32_t at = block_scan(max(want, 0), sum);
+        const int32_t want = i < n ? need(i) : 0;
+        const int64_t at = block_scan((int64_t)max(want, 0), sum);
         if (i < n) ws.first[i] = want < 0 ? -1 : (int32_t)min(wanted + at, (int64_t)0x7fffffff);
         wanted += sum;
     }
