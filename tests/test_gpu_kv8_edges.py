@@ -157,3 +157,48 @@ def test_output_and_queries_of_one_buffer():
         with pytest.raises(mr.MropeError, match="overlap"):
             mr.attend_kv8(big[q_at], i32(cu).cuda(), i32(ctx).cuda(), w.tables.cuda(), *w.cache(), out=big[o_at])
         assert torch.equal(big, kept)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_head_major_cache(dtype):
+    """A cache with its heads before its rows and a gap between pages."""
+    say("head-major", dtype)
+    w = World([200, 90], 32, 3, 128, seed=70)
+    turned = []
+    for x in w.cache()[:2]:
+        room = torch.zeros(w.nb, 3, 40, 128, dtype=torch.uint8, device="cuda")
+        y = room[:, :, :32].transpose(1, 2)
+        y.copy_(x.view(torch.uint8))
+        turned.append(y)
+    cache = (*turned, w.ks.cuda(), w.vs.cuda())
+    check(w, [0, 100, 130], [200, 90], w.heads(130, 6, dtype), dtype, 200, cache=cache)
+    check(w, None, [200, 90], w.heads(2, 6, dtype), dtype, 200, cache=cache)
+
+
+@pytest.mark.parametrize("q_len", [1, 60])
+def test_pool_past_two_gib(q_len):
+    """Pages past 2^31 bytes of a pool hold and give what the same pages of a small pool do, bit for bit."""
+    say("large pool", q_len)
+    w = World([150, 33], 64, 2, 256, seed=71)
+    big_n = 70000  # of 32 KB
+    move = big_n - w.nb
+    small = w.cache()
+    big = [torch.zeros(big_n, *x.shape[1:], dtype=torch.uint8 if x.dtype == F8 else x.dtype, device="cuda") for x in small]
+    for a, b in zip(big, small):
+        a[move:] = b.view(a.dtype)
+    far = torch.where(w.tables >= 0, w.tables + move, w.tables).cuda()
+    past = [150 - q_len, 33 - min(q_len, 33)]
+    cu = [0, 150 - past[0], 150 - past[0] + 33 - past[1]]
+    q, k, v = (w.heads(cu[-1], h, "bf16").cuda() for h in (8, 2, 2))
+    planes = torch.randint(0, 200, (3, cu[-1]), generator=w.g, dtype=torch.int32).cuda()
+    outs = []
+    for cache, tab in ((small, w.tables.cuda()), (big, far)):
+        qq = q.clone()
+        if q_len == 1:
+            mr.decode_kv8(qq, k, v, i32(past).cuda(), i32([0, 3]).cuda(), tab, *cache)
+        else:
+            mr.apply_kv8(qq, k, v, planes, i32(cu).cuda(), tab, *cache, pos_offset=i32(past).cuda())
+        outs.append(mr.attend_kv8(qq, None if q_len == 1 else i32(cu).cuda(), i32([150, 33]).cuda(), tab, *cache, return_lse=True))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    for a, b in zip(big, small):
+        assert torch.equal(a[move:], b.view(a.dtype)) and int(a[:move].count_nonzero()) == 0
