@@ -1,7 +1,9 @@
 // C ABI of the 8-bit paged K/V cache: argument checks and launches of the append, the attention and
 // the page calls.  The entry points are declared and documented in include/mrope.h.
+#include <algorithm>
 #include <cmath>
 #include <numeric>
+#include <utility>
 
 #include "mrope_kv8.h"
 #include "mrope_pages.h"
@@ -41,6 +43,22 @@ mrope_status check_kv8(const void *k_cache, const void *v_cache, const float *k_
         return fail(MROPE_ERR_ALIGN, "8-bit caches must be 16-byte aligned with strides that are multiples of 16");
     if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(tables, 4))
         return fail(MROPE_ERR_ALIGN, "scales and block_tables must be 4-byte aligned");
+    return MROPE_OK;
+}
+
+// An append writes every row of a page from one workgroup and pages from many: rows must lie apart (by the
+// strides in ascending order each past all rows of those before it).
+mrope_status check_rows_apart(int64_t num_blocks, int64_t c_block, int32_t block_size, int64_t c_tok, int32_t nk, int64_t c_head,
+                              int32_t head_dim)
+{
+    std::pair<int64_t, int64_t> dims[3] = {{c_block, num_blocks}, {c_tok, block_size}, {c_head, nk}};  // stride, extent
+    std::sort(dims, dims + 3);
+    int64_t span = head_dim;
+    for (const auto &d : dims) {
+        if (d.second <= 1) continue;
+        if (d.first < span) return fail(MROPE_ERR_ARG, "cache strides: rows overlap");
+        span += (d.second - 1) * d.first;
+    }
     return MROPE_OK;
 }
 
@@ -197,6 +215,8 @@ mrope_status mrope_apply_kv8(void *q, int64_t q_tok_stride, int64_t q_head_strid
     st = check_kv8(k_cache, v_cache, k_scale, v_scale, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
                    n_kv_heads, head_dim, block_tables, table_stride, table_width, n_seqs);
     if (st != MROPE_OK) return st;
+    st = check_rows_apart(num_blocks, cache_block_stride, block_size, cache_tok_stride, n_kv_heads, cache_head_stride, head_dim);
+    if (st != MROPE_OK) return st;
     if (n_tokens == 0) return MROPE_OK;
     if (!cu_seqlens) return fail(MROPE_ERR_ARG, "cu_seqlens is NULL");
     if (!planes) return fail(MROPE_ERR_ARG, "planes is NULL");
@@ -232,6 +252,8 @@ mrope_status mrope_decode_kv8(void *q, int64_t q_tok_stride, int64_t q_head_stri
     if (st != MROPE_OK) return st;
     st = check_kv8(k_cache, v_cache, k_scale, v_scale, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
                    n_kv_heads, head_dim, block_tables, table_stride, table_width, n_seqs);
+    if (st != MROPE_OK) return st;
+    st = check_rows_apart(num_blocks, cache_block_stride, block_size, cache_tok_stride, n_kv_heads, cache_head_stride, head_dim);
     if (st != MROPE_OK) return st;
     if (n_seqs == 0) return MROPE_OK;
     if (!pos || !amount) return fail(MROPE_ERR_ARG, "pos / amount is NULL");

@@ -334,7 +334,7 @@ mrope_status mrope_decode(void *q, int64_t q_tok_stride, int64_t q_head_stride, 
  *            written and not attended to.
  * block_size 16, 32 or 64.  head_dim 64, 128 or 256.  n_kv_heads 1..64.
  * Alignment: caches 16-byte aligned, cache strides multiples of 16 bytes.  The caches and scales must
- *            not overlap q, k, v or out.
+ *            not overlap q, k, v or out, and the rows of a cache that is appended to not one another.
  *
  * What an append writes.  A call that writes positions [a, b) of a sequence into a page, in which the
  * sequence already holds the h positions before a, gives the page (for K and for V, for each head)

@@ -2,7 +2,7 @@
 only, nothing is launched."""
 import pytest
 
-from test_kv8_abi_cpu import A, ARG, _attend, lib  # noqa: F401
+from test_kv8_abi_cpu import A, ARG, OK, _apply, _attend, _decode, lib  # noqa: F401
 
 H, T = 512, 4096  # bytes of a head (256 of bf16) and of a token of eight
 
@@ -19,3 +19,22 @@ H, T = 512, 4096  # bytes of a head (256 of bf16) and of a token of eight
 def test_attend_refuses_an_output_over_its_queries(lib, kw):  # noqa: F811
     assert _attend(lib, **kw) == ARG
     assert "overlap" in lib.mrope_last_error().decode()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(cb=0), dict(cb=256), dict(cb=8192 - 16), dict(cb=4096), dict(ct=256), dict(ch=512), dict(ct=496), dict(cb=512, ct=8192),
+    dict(ch=4096, ct=256, cb=4096), dict(cb=1 << 20, ch=16 * 256 - 16, ct=256),
+])
+def test_appends_refuse_rows_that_overlap(lib, kw):  # noqa: F811
+    for call in (_apply, _decode):
+        assert call(lib, **kw) == ARG
+        assert "overlap" in lib.mrope_last_error().decode()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(ch=4096, ct=256), dict(cb=512, ct=512 * 64), dict(cb=256, ct=2 * 64 * 256, ch=64 * 256), dict(nb=1, cb=0),
+    dict(nk=1, ch=0, cb=8192), dict(nk=1, ch=256, ct=256, cb=4096), dict(cb=1 << 40), dict(nb=0, cb=0),
+])
+def test_appends_take_any_order_of_the_dims(lib, kw):  # noqa: F811
+    """(No tokens: what is checked is checked, and nothing is launched.)"""
+    assert _apply(lib, n=0, **kw) == OK and _decode(lib, ns=0, **kw) == OK
