@@ -116,8 +116,8 @@ __device__ __forceinline__ int32_t chunk_of(int32_t lim, int n_chunks, int unit)
 // two) applied by the conversion.
 //
 // Bound: the cache's bytes, 2*D a token and KV head.  Measured, bf16, 8 query and 2 KV heads of 256: 64
-// sequences of 4,096 positions 44.8 us and 8 of 32,768 45.4, 269 MB at 6.0 and 5.9 TB/s (a plain read of that
-// size reaches 6.1), the join 4.7 and 5.7 us more; a matrix instruction is busy a tenth of the time.
+// sequences of 4,096 positions 45.0 us and 8 of 32,768 45.0, 269 MB at 6.0 TB/s (a plain read of that
+// size reaches 6.1), the join 4.8 and 5.6 us more; a matrix instruction is busy a tenth of the time.
 template <int NT>
 constexpr int kRowsOf = NT == 2 ? 8 : 4;
 constexpr int kFewWaves = 4;
@@ -658,14 +658,14 @@ __global__ __launch_bounds__(64 * kFewWaves, few_resident(D)) void attend_few_ke
 // As in the kernel for few rows S^T leaves a lane with the scores of one row, here for 32 of the 64 keys,
 // and O^T takes them from there: a step of 16 keys takes 8*a + 4*h + b, a < 2, b < 4, of lane half h.  V goes to
 // LDS transposed in that order, a dim's 64 keys in 128 bytes; its 16-byte pieces are swapped by the dim
-// (vswap) and 128 bytes left free every D/16 dims, which keeps the lanes of a read cycle and of a write in
-// different banks.  K's rows are 16 bytes longer for the same reason.  V is written a tile later than K, while
+// (vswap) and 128 bytes left free every D/16 dims, so that the lanes of a read cycle and of a write lie in
+// different banks (two other swaps took the same time).  K's rows are 16 bytes longer for the same reason.  V is written a tile later than K, while
 // the scores of its own tile are taken, and read in the next: two buffers of each are enough.
 //
 // Measured: 8 prompts of 4,096 tokens, bf16, 8 query and 2 KV heads of 256: 871 us, 0.63 PFLOP/s (550 GFLOP; with
 // the second term of P the matrix instructions do 825, 0.95 PFLOP/s, where a large bf16 product reaches 1.22
-// here).  With one wave a SIMD a tile of 64 tokens takes some 7,100 cycles (first and last steps included), of
-// which the matrix instructions need 3,456: without the softmax's arithmetic it took 807 us, without the
+// here).  With one wave a SIMD a tile of 64 tokens takes some 7,600 cycles (first and last steps included); the
+// matrix unit is busy for 3,100 of them.  Without the softmax's arithmetic it took 807 us, without the
 // reads of V 843, without its staging 812, with one term of P 734.  A second wave does not fit (192 registers
 // of sums and queries).
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -776,10 +776,10 @@ __device__ __forceinline__ int32_t wave_sum(int32_t x)
 }
 
 // The tile of the rank-th longest context, and its number w: workgroups start in this order, so that a long
-// one does not begin when the others end (4 prompts of 1,500 tokens, bf16, D = 256: 117 us in the order
-// of the batch, 86 so; 8 of 4,096: 868 and 738).  Tile k of a sequence is ranked by past + floor(R (k + 1) / g); the rank-th
+// one does not begin when the others end (4 prompts of 1,500 tokens, bf16, D = 256: 126 us from the batch's last
+// tile on, 98 so; 8 of 4,096: 917 and 900).  Tile k of a sequence is ranked by past + floor(R (k + 1) / g); the rank-th
 // largest of these is searched for, a sequence a lane.  Batches of more sequences than lanes start from the last
-// tile: with so many the ends are small.
+// tile.
 template <int R>
 __device__ __forceinline__ bool find_long_tile(const Attend &a, int g, int64_t rank, int64_t n_tiles, int lane, Tile &t, int64_t &w)
 {
@@ -1395,8 +1395,11 @@ struct Plan {
 
 // Tiles of many rows where a sequence's rows of a KV head would fill more than four tiles of few rows, which
 // read the cache once each.  Measured (us, few against many; bf16, 8 query and 2 KV heads of 256): 3
-// sequences with 20,000 tokens behind them, 16 rows each 30 / 35, 32 rows 38 / 36, 48 rows 79 / 43; 16
-// sequences with 1,500, 32 rows 28 / 36, 48 rows 45 / 40.  fp32 (4 rows a tile): 16 rows 44 / 69, 24 rows 89 / 70.
+// sequences with 20,000 tokens behind them, 16 rows each 30 / 43, 32 rows 40 / 43, 48 rows 79 / 46; 16
+// sequences with 1,500, 32 rows 28 / 32, 48 rows 44 / 33.  fp32 (4 rows a tile): 16 rows 43 / 66, 24 rows 90 / 68.
+// The host does not see lengths: the rule takes the call's average, and a call that mixes prompts with
+// single tokens has one kernel for both (one prompt of 2,048 tokens and seven tokens at 100,000 positions:
+// 4.2 ms together, 0.09 and 0.14 in calls of their own; one of 4,096 and a thousand at 500: 0.64, and 0.21 and 0.15).
 constexpr int64_t kFewTiles = 4;
 Plan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io, bool one_token,
                int32_t table_width, int32_t block_size)
@@ -1410,9 +1413,9 @@ Plan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t
     const int64_t unit = p.many ? kManyUnit : kFewUnit, most = (cap + unit - 1) / unit;
     const size_t part = (size_t)(p.rows * (head_dim + 2) * 4) * nk;
     if (p.many) {
-        // The context is cut where the tiles are fewer than the compute units; twice as many chunks took 57 us
-        // where these take 44 (3 sequences of 16 tokens behind 20,011, bf16, D = 256), and two or three a
-        // compute unit, which D = 128 and 64 have room for, 46 and 40 us for 42 and 36 (2 of 300 behind 500).
+        // The context is cut where the tiles are fewer than the compute units; twice as many chunks took 63 us
+        // where these take 48 (3 sequences of 16 tokens behind 20,011, bf16, D = 256), and two a compute unit,
+        // which D = 128 and 64 have room for, 37 and 30 us for 33 and 26 (2 of 300 behind 500).
         // (Of the tiles in the grid those are counted that sequences of equal lengths would have.)
         const int64_t fill = 256, seq_rows = (n_tokens * g + n_seqs - 1) / n_seqs;
         const int64_t likely = std::min(p.tiles, n_seqs * ((seq_rows + p.rows - 1) / p.rows));

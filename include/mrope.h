@@ -401,6 +401,8 @@ mrope_status mrope_decode_kv8(void *q, int64_t q_tok_stride, int64_t q_head_stri
  *            fp32, whatever else the call holds.  The sum over p_j v_j is held 2^8 smaller, p_j as parts of the
  *            largest: that has to stay below fp32's largest value.
  *            What a row does not see reaches it in no way, NaN codes among it.
+ *            One kernel serves a call, chosen by its average rows a sequence: prompts and single tokens with
+ *            long contexts are faster in calls of their own than together.
  * workspace  256-byte aligned device memory of mrope_attend_kv8_workspace_bytes(...) bytes (0: may be
  *            NULL), needing no initialisation; calls that share one must be ordered.
  *            one_token: whether cu_seqlens is NULL.
