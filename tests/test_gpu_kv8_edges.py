@@ -222,3 +222,43 @@ def test_prompts_with_nan_values(dtype, D, n_seqs):
     raw[hit] = torch.tensor([0x7f, 0xff], dtype=torch.uint8)[torch.randint(0, 2, (int(hit.sum()),), generator=w.g)]
     cu = [n * s for s in range(n_seqs + 1)]
     check(w, cu, ctx, w.heads(cu[-1], 6, dtype), dtype, max(ctx), what=n_seqs)
+
+
+def test_prompts_captured_and_on_two_streams():
+    """Pieces of prompts (cut and joined, and whole) in a graph, replayed with other inputs and eager work between
+    the replays; two such calls at once on streams of their own."""
+    say("prompts captured")
+    w = World([2100, 900], 16, 2, 128, seed=90)
+    tab, cache = w.tables.cuda(), w.cache()
+    cu, ctx = i32([0, 40, 130]).cuda(), i32([2100, 900]).cuda()
+    q = w.heads(130, 8, "bf16").cuda()
+    out, lse = torch.empty_like(q), torch.empty(130, 8, device="cuda")
+
+    def call():
+        mr.attend_kv8(q, cu, ctx, tab, *cache, out=out, lse=lse)
+
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for i in range(4):
+        q.copy_(w.heads(130, 8, "bf16"))
+        call()
+        want = out.clone(), lse.clone()
+        out.zero_(), lse.zero_()
+        torch.ones(1 << 20, device="cuda").sum().item()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), i
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    inputs = [w.heads(130, 8, "bf16").cuda() for _ in range(2)]
+    want = [mr.attend_kv8(x, cu, ctx, tab, *cache)[0].clone() for x in inputs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(mr.attend_kv8(inputs[k], cu, ctx, tab, *cache)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[k]) for k in range(2) for x in got[k])
