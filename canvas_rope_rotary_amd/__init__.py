@@ -20,6 +20,9 @@ the Qwen3.5 hybrid, on Core AI", section "The canvas rule and why the gate is on
 * ``apply_kv8`` / ``decode_kv8``  the cache writes for a cache held in 8 bits (e4m3 codes, one
                 power-of-two scale for each page and KV head), placed by block tables;
 * ``attend_kv8``  causal attention over that cache, for prompts, pieces of prompts and decode steps;
+* ``planes_tree`` / ``attend_tree_kv8`` / ``verify_tree`` / ``keep_kv8``  a step of generation with trees of
+                drafted tokens over that cache: their planes and masks, attention under the masks, which
+                drafts the target accepts, and the accepted path's rows moved together;
 * ``pages_grow`` / ``pages_free`` / ``pages_fork`` / ``pages_compact`` / ``pages_copy``  the pages of
                 paged caches: reference counts, block tables and the copies they imply.
 """
@@ -33,10 +36,15 @@ from ._lib import (MROPE_BF16, MROPE_F16, MROPE_F32, MarkerFlags, MropeError, TE
 from ._kv8 import (PAGES_BAD_ROW, PAGES_NOT_ENOUGH, apply_kv8, attend_kv8, attend_kv8_workspace_bytes, decode_kv8,
                    pages_compact, pages_copy, pages_fork, pages_free, pages_grow)
 
+from ._tree import (MAX_LAYERS, TREE_MAX_TOKENS, attend_tree_kv8, attend_tree_kv8_workspace_bytes, keep_kv8, planes_tree,
+                    verify_tree)
+
 IMAGE_ID = 248078
 DEFAULT_THETA = 1e7
 
 __all__ = ["planes", "apply", "apply_ids", "apply_ids_noalloc", "apply_kv", "apply_ids_kv", "decode", "Workspace", "MropeError", "MarkerFlags",
            "check_slots", "prepare", "PreparedCall", "cu_seqlens_from_lens", "library_path", "IMAGE_ID", "DEFAULT_THETA", "TEXT_ONLY_START",
            "MROPE_F32", "MROPE_BF16", "MROPE_F16", "apply_kv8", "decode_kv8", "attend_kv8", "attend_kv8_workspace_bytes",
-           "pages_grow", "pages_free", "pages_fork", "pages_compact", "pages_copy", "PAGES_NOT_ENOUGH", "PAGES_BAD_ROW"]
+           "pages_grow", "pages_free", "pages_fork", "pages_compact", "pages_copy", "PAGES_NOT_ENOUGH", "PAGES_BAD_ROW",
+           "planes_tree", "attend_tree_kv8", "attend_tree_kv8_workspace_bytes", "verify_tree", "keep_kv8", "TREE_MAX_TOKENS",
+           "MAX_LAYERS"]

@@ -24,7 +24,9 @@ EXPORTS = ("mrope_abi_version", "mrope_status_string", "mrope_last_error", "mrop
            "mrope_apply_kv",
            "mrope_apply_ids_kv", "mrope_decode", "mrope_apply_kv8", "mrope_decode_kv8",
            "mrope_attend_kv8_workspace_bytes", "mrope_attend_kv8", "mrope_pages_workspace_bytes", "mrope_pages_grow",
-           "mrope_pages_free", "mrope_pages_fork", "mrope_pages_compact", "mrope_pages_copy")
+           "mrope_pages_free", "mrope_pages_fork", "mrope_pages_compact", "mrope_pages_copy", "mrope_planes_tree",
+           "mrope_attend_tree_kv8_workspace_bytes", "mrope_attend_tree_kv8", "mrope_verify_tree_workspace_bytes",
+           "mrope_verify_tree", "mrope_keep_kv8")
 
 
 HOOK_FUSED_CHUNKED = 1
@@ -114,6 +116,19 @@ def load():
     lib.mrope_attend_kv8_workspace_bytes.restype = U64
     lib.mrope_attend_kv8.argtypes = [*heads, I64, I32, I32, I32, P, I32, P, *tables, *kv8, F64, P, I64, I64, P, P, U64, P]
     lib.mrope_attend_kv8.restype = ctypes.c_int
+    lib.mrope_planes_tree.argtypes = [P, I64, P, I32, P, P, P, I64, P, I32, P]
+    lib.mrope_planes_tree.restype = ctypes.c_int
+    lib.mrope_attend_tree_kv8_workspace_bytes.argtypes = [I64, I32, I32, I32, I32, I32, I32, I32]
+    lib.mrope_attend_tree_kv8_workspace_bytes.restype = U64
+    lib.mrope_attend_tree_kv8.argtypes = [*heads, I64, I32, I32, I32, P, I32, P, P, I32, *tables, *kv8, F64, P, I64, I64, P, P,
+                                          U64, P]
+    lib.mrope_attend_tree_kv8.restype = ctypes.c_int
+    lib.mrope_verify_tree_workspace_bytes.argtypes = [I32, I32, I32, I32]
+    lib.mrope_verify_tree_workspace_bytes.restype = U64
+    lib.mrope_verify_tree.argtypes = [P, I64, P, I64, I32, I32, I64, P, P, P, I32, P, P, P, P, P, P, U64, P]
+    lib.mrope_verify_tree.restype = ctypes.c_int
+    lib.mrope_keep_kv8.argtypes = [P, I32, I32, I32, *kv8[4:], P, P, I64, P, I32, P, *tables, P]
+    lib.mrope_keep_kv8.restype = ctypes.c_int
     lib.mrope_pages_workspace_bytes.argtypes = [I64, I64]
     lib.mrope_pages_workspace_bytes.restype = U64
     state = [P, I64, *tables, P, I64]  # refcount, num_blocks, tables, seq_lens, n_rows

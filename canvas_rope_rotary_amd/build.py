@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmrope.so")
 OBJ = os.path.join(PKG, "_build")
 SOURCES = ["mrope_kernels.hip", "mrope_abi.hip", "mrope_append.hip", "mrope_attend.hip", "mrope_pages.hip",
-           "mrope_kv8_abi.hip"]
+           "mrope_attend_tree.hip", "mrope_tree.hip", "mrope_verify.hip", "mrope_kv8_abi.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

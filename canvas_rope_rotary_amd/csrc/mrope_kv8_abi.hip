@@ -1,5 +1,5 @@
-// C ABI of the 8-bit paged K/V cache: argument checks and launches of the append, the attention and
-// the page calls.  The entry points are declared and documented in include/mrope.h.
+// C ABI of the 8-bit paged K/V cache: argument checks and launches of the append, the attention, the
+// page calls and the calls for trees of drafted tokens.  The entry points are declared and documented in include/mrope.h.
 #include <algorithm>
 #include <cmath>
 #include <numeric>
@@ -7,6 +7,7 @@
 
 #include "mrope_kv8.h"
 #include "mrope_pages.h"
+#include "mrope_tree.h"
 
 using namespace mrope;
 
@@ -143,6 +144,96 @@ Append make_append(void *q, int64_t q_tok, int64_t q_head, int32_t nq, const voi
     a.n_seqs = n_seqs;
     a.kv = kv;
     return a;
+}
+
+mrope_status check_workspace(const void *ws, size_t bytes, size_t need)
+{
+    if (need == 0) return MROPE_OK;
+    if (!ws) return fail(MROPE_ERR_WORKSPACE, "workspace is NULL");
+    if (!aligned(ws, 256)) return fail(MROPE_ERR_WORKSPACE, "workspace not 256-byte aligned");
+    if (bytes < need) return fail(MROPE_ERR_WORKSPACE, "workspace too small (%zu < %zu)", bytes, need);
+    return MROPE_OK;
+}
+
+// An attention call's arguments; fills `a` (a.n_tokens == 0: nothing to do).
+mrope_status check_attend(const void *q, int64_t q_tok_stride, int64_t q_head_stride, int32_t n_q_heads,
+                              int64_t n_tokens, int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                              const int32_t *cu_seqlens, int32_t n_seqs, const int32_t *context_lens,
+                              const int32_t *block_tables, int64_t table_stride, int32_t table_width, const void *k_cache,
+                              const void *v_cache, const float *k_scale, const float *v_scale, int32_t block_size,
+                              int64_t num_blocks, int64_t cache_block_stride, int64_t cache_tok_stride,
+                              int64_t cache_head_stride, double softmax_scale, void *out, int64_t out_tok_stride,
+                              int64_t out_head_stride, float *lse, void *workspace, size_t workspace_bytes,
+                          bool tree, Attend &a)
+{
+    mrope_status st = check_kv8_shape(n_kv_heads, head_dim, block_size);
+    if (st != MROPE_OK) return st;
+    if (n_q_heads <= 0 || n_q_heads > kMaxHeads || n_q_heads % n_kv_heads)
+        return fail(MROPE_ERR_UNSUPPORTED, "n_q_heads must be a multiple of n_kv_heads in [1, %d] (got %d, %d)", kMaxHeads,
+                    n_q_heads, n_kv_heads);
+    // Q, then the output in the place of K heads of the same count
+    st = check_heads(const_cast<void *>(q), q_tok_stride, q_head_stride, n_q_heads, out, out_tok_stride, out_head_stride,
+                     n_q_heads, n_tokens, head_dim, 64, dtype, nullptr, nullptr);
+    if (st != MROPE_OK) return st;
+    if (n_seqs < 0) return fail(MROPE_ERR_ARG, "n_seqs < 0");
+    if (n_seqs == 0 && n_tokens > 0) return fail(MROPE_ERR_ARG, "tokens given but no sequences");
+    if (!tree && !cu_seqlens && n_tokens != n_seqs) return fail(MROPE_ERR_ARG, "without cu_seqlens there is one token a sequence");
+    const float scale_log2 = (float)(softmax_scale * 1.4426950408889634);
+    if (!std::isfinite(scale_log2)) return fail(MROPE_ERR_ARG, "softmax_scale must be finite (in fp32)");
+    st = check_kv8(k_cache, v_cache, k_scale, v_scale, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
+                   n_kv_heads, head_dim, block_tables, table_stride, table_width, n_seqs);
+    if (st != MROPE_OK) return st;
+    if (!aligned(lse, 4)) return fail(MROPE_ERR_ALIGN, "lse must be 4-byte aligned");
+    // a tile has 256 threads, and at least 4 rows, or 128 in a grid of all KV heads
+    const int64_t group = n_q_heads / n_kv_heads;
+    if ((n_tokens * ((group + 3) / 4) + n_seqs + 1024) * 256 > kMaxGridThreads ||
+        (n_tokens * group / 128 + n_seqs) * n_kv_heads * 256 > kMaxGridThreads)
+        return fail(MROPE_ERR_ARG, "too many query rows (%lld tokens, %d heads a KV head)", (long long)n_tokens, (int)group);
+    if ((int64_t)table_width * block_size > kMaxContext)
+        return fail(MROPE_ERR_ARG, "block_tables: at most 2^27 positions a sequence (got %lld)", (long long)table_width * block_size);
+    a = Attend{};
+    if (n_tokens == 0) return MROPE_OK;
+    if (tree && !cu_seqlens) return fail(MROPE_ERR_ARG, "cu_seqlens is NULL");
+    if (!context_lens) return fail(MROPE_ERR_ARG, "context_lens is NULL");
+    const int32_t width = num_blocks > 0 ? table_width : 0;
+    const size_t need =
+        tree ? mrope_attend_tree_kv8_workspace_bytes(n_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, dtype, width, block_size)
+             : mrope_attend_kv8_workspace_bytes(n_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, dtype, cu_seqlens == nullptr,
+                                                width, block_size);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != MROPE_OK) return st;
+    if (heads_overlap(q, q_tok_stride, q_head_stride, out, out_tok_stride, out_head_stride, n_q_heads, n_tokens, head_dim,
+                      dtype == MROPE_F32 ? 4 : 2))
+        return fail(MROPE_ERR_ARG, "out must not overlap q");
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.q_tok = q_tok_stride;
+    a.q_head = q_head_stride;
+    a.o_tok = out_tok_stride;
+    a.o_head = out_head_stride;
+    a.nq = n_q_heads;
+    a.head_dim = head_dim;
+    a.n_tokens = n_tokens;
+    a.cu = cu_seqlens;
+    a.n_seqs = n_seqs;
+    a.ctx = context_lens;
+    a.scale_log2 = scale_log2;
+    a.workspace = workspace;
+    a.kv = make_kv8(k_cache, v_cache, k_scale, v_scale, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
+                    n_kv_heads, block_tables, table_stride, table_width, block_size);
+    return MROPE_OK;
+}
+
+
+// Packed trees: their tokens and where each sequence's begin.
+mrope_status check_trees(int64_t n_tokens, const int32_t *cu_seqlens, int32_t n_seqs)
+{
+    if (n_tokens < 0 || n_tokens > 0x7ffffffe) return fail(MROPE_ERR_ARG, "n_tokens out of range (%lld)", (long long)n_tokens);
+    if (n_seqs < 0) return fail(MROPE_ERR_ARG, "n_seqs < 0");
+    if (n_seqs == 0 && n_tokens > 0) return fail(MROPE_ERR_ARG, "tokens given but no sequences");
+    if (!aligned(cu_seqlens, 4)) return fail(MROPE_ERR_ALIGN, "cu_seqlens must be 4-byte aligned");
+    if (n_tokens > 0 && !cu_seqlens) return fail(MROPE_ERR_ARG, "cu_seqlens is NULL");
+    return MROPE_OK;
 }
 
 // The state of the page calls; fills `p`.
@@ -287,63 +378,147 @@ mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_hea
                               int64_t cache_head_stride, double softmax_scale, void *out, int64_t out_tok_stride,
                               int64_t out_head_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream)
 {
-    mrope_status st = check_kv8_shape(n_kv_heads, head_dim, block_size);
-    if (st != MROPE_OK) return st;
-    if (n_q_heads <= 0 || n_q_heads > kMaxHeads || n_q_heads % n_kv_heads)
-        return fail(MROPE_ERR_UNSUPPORTED, "n_q_heads must be a multiple of n_kv_heads in [1, %d] (got %d, %d)", kMaxHeads,
-                    n_q_heads, n_kv_heads);
-    // Q, then the output in the place of K heads of the same count
-    st = check_heads(const_cast<void *>(q), q_tok_stride, q_head_stride, n_q_heads, out, out_tok_stride, out_head_stride,
-                     n_q_heads, n_tokens, head_dim, 64, dtype, nullptr, nullptr);
-    if (st != MROPE_OK) return st;
-    if (n_seqs < 0) return fail(MROPE_ERR_ARG, "n_seqs < 0");
-    if (n_seqs == 0 && n_tokens > 0) return fail(MROPE_ERR_ARG, "tokens given but no sequences");
-    if (!cu_seqlens && n_tokens != n_seqs) return fail(MROPE_ERR_ARG, "without cu_seqlens there is one token a sequence");
-    const float scale_log2 = (float)(softmax_scale * 1.4426950408889634);
-    if (!std::isfinite(scale_log2)) return fail(MROPE_ERR_ARG, "softmax_scale must be finite (in fp32)");
-    st = check_kv8(k_cache, v_cache, k_scale, v_scale, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
-                   n_kv_heads, head_dim, block_tables, table_stride, table_width, n_seqs);
-    if (st != MROPE_OK) return st;
-    if (!aligned(lse, 4)) return fail(MROPE_ERR_ALIGN, "lse must be 4-byte aligned");
-    // a tile has 256 threads, and at least 4 rows, or 128 in a grid of all KV heads
-    const int64_t group = n_q_heads / n_kv_heads;
-    if ((n_tokens * ((group + 3) / 4) + n_seqs + 1024) * 256 > kMaxGridThreads ||
-        (n_tokens * group / 128 + n_seqs) * n_kv_heads * 256 > kMaxGridThreads)
-        return fail(MROPE_ERR_ARG, "too many query rows (%lld tokens, %d heads a KV head)", (long long)n_tokens, (int)group);
-    if ((int64_t)table_width * block_size > kMaxContext)
-        return fail(MROPE_ERR_ARG, "block_tables: at most 2^27 positions a sequence (got %lld)", (long long)table_width * block_size);
-    if (n_tokens == 0) return MROPE_OK;
-    if (!context_lens) return fail(MROPE_ERR_ARG, "context_lens is NULL");
-    const size_t need = mrope_attend_kv8_workspace_bytes(n_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, dtype,
-                                                         cu_seqlens == nullptr, num_blocks > 0 ? table_width : 0, block_size);
-    if (need > 0) {
-        if (!workspace) return fail(MROPE_ERR_WORKSPACE, "workspace is NULL");
-        if (!aligned(workspace, 256)) return fail(MROPE_ERR_WORKSPACE, "workspace not 256-byte aligned");
-        if (workspace_bytes < need) return fail(MROPE_ERR_WORKSPACE, "workspace too small (%zu < %zu)", workspace_bytes, need);
-    }
-    if (heads_overlap(q, q_tok_stride, q_head_stride, out, out_tok_stride, out_head_stride, n_q_heads, n_tokens, head_dim,
-                      dtype == MROPE_F32 ? 4 : 2))
-        return fail(MROPE_ERR_ARG, "out must not overlap q");
-    Attend a{};
-    a.q = q;
-    a.out = out;
-    a.lse = lse;
-    a.q_tok = q_tok_stride;
-    a.q_head = q_head_stride;
-    a.o_tok = out_tok_stride;
-    a.o_head = out_head_stride;
-    a.nq = n_q_heads;
-    a.head_dim = head_dim;
-    a.n_tokens = n_tokens;
-    a.cu = cu_seqlens;
-    a.n_seqs = n_seqs;
-    a.ctx = context_lens;
-    a.scale_log2 = scale_log2;
-    a.workspace = workspace;
-    a.kv = make_kv8(k_cache, v_cache, k_scale, v_scale, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
-                    n_kv_heads, block_tables, table_stride, table_width, block_size);
+    Attend a;
+    const mrope_status st = check_attend(q, q_tok_stride, q_head_stride, n_q_heads, n_tokens, n_kv_heads, head_dim, dtype, cu_seqlens, n_seqs,
+                                         context_lens, block_tables, table_stride, table_width, k_cache, v_cache, k_scale, v_scale,
+                                         block_size, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
+                                         softmax_scale, out, out_tok_stride, out_head_stride, lse, workspace, workspace_bytes, false, a);
+    if (st != MROPE_OK || a.n_tokens == 0) return st;
     (void)hipGetLastError();
     return hip_status(launch_attend(a, dtype, static_cast<hipStream_t>(stream)), "mrope_attend_kv8");
+}
+
+size_t mrope_attend_tree_kv8_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                             int32_t head_dim, int32_t dtype, int32_t table_width, int32_t block_size)
+{
+    (void)dtype;
+    if (n_tokens <= 0 || n_seqs <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads || table_width <= 0 ||
+        block_size <= 0)
+        return 0;
+    return attend_tree_workspace_bytes(n_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, table_width, block_size);
+}
+
+mrope_status mrope_attend_tree_kv8(const void *q, int64_t q_tok_stride, int64_t q_head_stride, int32_t n_q_heads,
+                                   int64_t n_tokens, int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                                   const int32_t *cu_seqlens, int32_t n_seqs, const int32_t *context_lens,
+                                   const uint64_t *mask, int32_t mask_words, const int32_t *block_tables,
+                                   int64_t table_stride, int32_t table_width, const void *k_cache, const void *v_cache,
+                                   const float *k_scale, const float *v_scale, int32_t block_size, int64_t num_blocks,
+                                   int64_t cache_block_stride, int64_t cache_tok_stride, int64_t cache_head_stride,
+                                   double softmax_scale, void *out, int64_t out_tok_stride, int64_t out_head_stride,
+                                   float *lse, void *workspace, size_t workspace_bytes, void *stream)
+{
+    AttendTree a;
+    mrope_status st = check_trees(n_tokens, cu_seqlens, n_seqs);
+    if (st != MROPE_OK) return st;
+    st = check_attend(q, q_tok_stride, q_head_stride, n_q_heads, n_tokens, n_kv_heads, head_dim, dtype, cu_seqlens, n_seqs,
+                                         context_lens, block_tables, table_stride, table_width, k_cache, v_cache, k_scale, v_scale,
+                                         block_size, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
+                                         softmax_scale, out, out_tok_stride, out_head_stride, lse, workspace, workspace_bytes, true, a);
+    if (st != MROPE_OK) return st;
+    if (mask_words < 1 || mask_words > 64) return fail(MROPE_ERR_ARG, "mask_words must be in [1, 64] (got %d)", mask_words);
+    if (!aligned(mask, 8) || !aligned(context_lens, 4)) return fail(MROPE_ERR_ALIGN, "mask must be 8-byte, context_lens 4-byte aligned");
+    if (a.n_tokens == 0) return MROPE_OK;
+    if (!mask) return fail(MROPE_ERR_ARG, "mask is NULL");
+    a.mask = mask;
+    a.mask_words = mask_words;
+    (void)hipGetLastError();
+    return hip_status(launch_attend_tree(a, dtype, static_cast<hipStream_t>(stream)), "mrope_attend_tree_kv8");
+}
+
+mrope_status mrope_planes_tree(const int32_t *parents, int64_t n_tokens, const int32_t *cu_seqlens, int32_t n_seqs,
+                               const int32_t *pos_offset, const int32_t *amount, int32_t *planes, int64_t plane_stride,
+                               uint64_t *mask, int32_t mask_words, void *stream)
+{
+    mrope_status st = check_trees(n_tokens, cu_seqlens, n_seqs);
+    if (st != MROPE_OK) return st;
+    if (mask_words < 1 || mask_words > kTreeTokens / 64)
+        return fail(MROPE_ERR_ARG, "mask_words must be in [1, %d] (got %d)", kTreeTokens / 64, mask_words);
+    if (plane_stride < n_tokens) return fail(MROPE_ERR_ARG, "plane_stride < n_tokens");
+    if (!aligned(parents, 4) || !aligned(pos_offset, 4) || !aligned(amount, 4) || !aligned(planes, 4) || !aligned(mask, 8))
+        return fail(MROPE_ERR_ALIGN, "int32 arrays must be 4-byte aligned, mask 8-byte aligned");
+    if ((int64_t)n_seqs * 256 > kMaxGridThreads) return fail(MROPE_ERR_ARG, "too many sequences (%d)", n_seqs);
+    if (n_tokens == 0) return MROPE_OK;
+    if (!parents || !pos_offset || !planes || !mask) return fail(MROPE_ERR_ARG, "parents / pos_offset / planes / mask is NULL");
+    const PlanesTree a{parents, cu_seqlens, n_seqs, n_tokens, pos_offset, amount, planes, plane_stride, mask, mask_words};
+    (void)hipGetLastError();
+    return hip_status(launch_planes_tree(a, static_cast<hipStream_t>(stream)), "mrope_planes_tree");
+}
+
+size_t mrope_verify_tree_workspace_bytes(int32_t n_seqs, int32_t vocab, int32_t has_draft, int32_t has_parents)
+{
+    if (n_seqs <= 0 || vocab <= 0) return 0;
+    return verify_ws_bytes(n_seqs, verify_plan(n_seqs, vocab, has_draft && has_parents));
+}
+
+mrope_status mrope_verify_tree(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,
+                               int32_t vocab, int32_t dtype, int64_t n_tokens, const int32_t *ids, const int32_t *parents,
+                               const int32_t *cu_seqlens, int32_t n_seqs, const float *u_accept, const float *u_next,
+                               int32_t *n_kept, int32_t *path, int32_t *next_ids, void *workspace, size_t workspace_bytes,
+                               void *stream)
+{
+    mrope_status st = check_trees(n_tokens, cu_seqlens, n_seqs);
+    if (st != MROPE_OK) return st;
+    if (dtype != MROPE_F32 && dtype != MROPE_BF16 && dtype != MROPE_F16) return fail(MROPE_ERR_UNSUPPORTED, "unknown dtype %d", dtype);
+    if (vocab < 1) return fail(MROPE_ERR_ARG, "vocab must be > 0 (got %d)", vocab);
+    if (target_stride < vocab || (draft && draft_stride < vocab)) return fail(MROPE_ERR_ARG, "target / draft stride < vocab");
+    const unsigned elem = dtype == MROPE_F32 ? 4 : 2;
+    if (!aligned(target, elem) || !aligned(draft, elem)) return fail(MROPE_ERR_ALIGN, "target / draft must be aligned to their elements");
+    if (!aligned(ids, 4) || !aligned(parents, 4) || !aligned(u_accept, 4) || !aligned(u_next, 4) || !aligned(n_kept, 4) ||
+        !aligned(path, 4) || !aligned(next_ids, 4))
+        return fail(MROPE_ERR_ALIGN, "int32 and fp32 arrays must be 4-byte aligned");
+    if (n_seqs == 0) return MROPE_OK;
+    const VerifyPlan plan = verify_plan(n_seqs, vocab, draft && parents);
+    if ((int64_t)n_seqs * plan.n_chunks * 256 > kMaxGridThreads)
+        return fail(MROPE_ERR_ARG, "too many sequences for the vocabulary (%d, %d)", n_seqs, vocab);
+    if (!n_kept || !next_ids || !u_next || !cu_seqlens) return fail(MROPE_ERR_ARG, "cu_seqlens / u_next / n_kept / next_ids is NULL");
+    if (n_tokens > 0 && (!target || !ids || !u_accept || !path)) return fail(MROPE_ERR_ARG, "target / ids / u_accept / path is NULL");
+    if ((st = check_workspace(workspace, workspace_bytes, verify_ws_bytes(n_seqs, plan))) != MROPE_OK) return st;
+    const Verify a{target, draft, target_stride, draft_stride, vocab, ids, parents, cu_seqlens, n_seqs, n_tokens,
+                   u_accept, u_next, n_kept, path, next_ids};
+    (void)hipGetLastError();
+    return hip_status(launch_verify(a, dtype, plan, workspace, static_cast<hipStream_t>(stream)), "mrope_verify_tree");
+}
+
+mrope_status mrope_keep_kv8(const mrope_kv8_layer *layers, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
+                            int32_t block_size, int64_t num_blocks, int64_t cache_block_stride, int64_t cache_tok_stride,
+                            int64_t cache_head_stride, const int32_t *n_kept, const int32_t *path, int64_t n_tokens,
+                            const int32_t *cu_seqlens, int32_t n_seqs, const int32_t *pos_offset,
+                            const int32_t *block_tables, int64_t table_stride, int32_t table_width, void *stream)
+{
+    mrope_status st = check_kv8_shape(n_kv_heads, head_dim, block_size);
+    if (st != MROPE_OK) return st;
+    if ((st = check_trees(n_tokens, cu_seqlens, n_seqs)) != MROPE_OK) return st;
+    if (n_layers < 0 || n_layers > MROPE_MAX_LAYERS) return fail(MROPE_ERR_ARG, "n_layers must be in [0, %d] (got %d)", MROPE_MAX_LAYERS, n_layers);
+    if (n_layers > 0 && !layers) return fail(MROPE_ERR_ARG, "layers is NULL");
+    KeepLayers set{};
+    for (int32_t i = 0; i < n_layers; ++i) {
+        const mrope_kv8_layer &l = set.at[i] = layers[i];
+        st = check_kv8(l.k_cache, l.v_cache, l.k_scale, l.v_scale, num_blocks, cache_block_stride, cache_tok_stride,
+                       cache_head_stride, n_kv_heads, head_dim, block_tables, table_stride, table_width, n_seqs);
+        if (st != MROPE_OK) return st;
+    }
+    st = check_rows_apart(num_blocks, cache_block_stride, block_size, cache_tok_stride, n_kv_heads, cache_head_stride, head_dim);
+    if (st != MROPE_OK) return st;
+    if (!aligned(n_kept, 4) || !aligned(path, 4) || !aligned(pos_offset, 4))
+        return fail(MROPE_ERR_ALIGN, "n_kept, path and pos_offset must be 4-byte aligned");
+    if (((int64_t)n_seqs * n_layers * 2 * n_kv_heads + 3) / 4 * 256 > kMaxGridThreads)
+        return fail(MROPE_ERR_ARG, "too many sequences for the layers and heads (%d)", n_seqs);
+    if (n_tokens == 0 || n_layers == 0) return MROPE_OK;
+    if (!n_kept || !path || !pos_offset) return fail(MROPE_ERR_ARG, "n_kept / path / pos_offset is NULL");
+    Keep a{};
+    a.n_kept = n_kept;
+    a.path = path;
+    a.cu = cu_seqlens;
+    a.n_seqs = n_seqs;
+    a.n_tokens = n_tokens;
+    a.pos = pos_offset;
+    a.n_layers = n_layers;
+    a.head_dim = head_dim;
+    a.kv = make_kv8(nullptr, nullptr, nullptr, nullptr, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
+                    n_kv_heads, block_tables, table_stride, table_width, block_size);
+    (void)hipGetLastError();
+    return hip_status(launch_keep(a, set, static_cast<hipStream_t>(stream)), "mrope_keep_kv8");
 }
 
 size_t mrope_pages_workspace_bytes(int64_t num_blocks, int64_t n_rows)

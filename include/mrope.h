@@ -420,6 +420,121 @@ mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_hea
                               int64_t out_head_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Trees of drafted tokens (mrope_planes_tree, mrope_attend_tree_kv8, mrope_verify_tree, mrope_keep_kv8).
+ *
+ * A step of generation with a drafter: each sequence brings a tree of tokens.  Its token 0 is the token that was
+ * accepted last and is not in the cache yet; the others are drafts.  The step takes the tree's planes and mask, for
+ * each layer rotates and appends all tokens at the positions after the context (mrope_apply_kv8 with these planes
+ * and pos_offset) and attends under the mask, verifies the drafts against the target's distributions, and
+ * keeps the accepted path: its rows move together, and the next step appends after them.
+ *
+ * cu_seqlens [n_seqs + 1] int32: the tokens of each sequence, as in mrope_planes; empty trees are allowed, and
+ *            tokens behind cu_seqlens[n_seqs] are left as they are in every output.
+ * parents    [n_tokens] int32: the index, within its sequence, of each token's parent, which comes before it.  A
+ *            value outside [0, i) for token i: it has none.
+ * Of a tree, the first MROPE_TREE_MAX_TOKENS tokens have parents and can be accepted.
+ * ------------------------------------------------------------------------------------------- */
+#define MROPE_TREE_MAX_TOKENS 1024
+
+/* ---------------------------------------------------------------------------------------------
+ * mrope_planes_tree -- planes and masks of trees ([card] canvas table, last row: generated tokens take p - amount on
+ * all three planes; a drafted token's p is its distance from the root on top of the root's).
+ *
+ * pos_offset [n_seqs] int32: the position of each sequence's token 0.  amount [n_seqs] int32, nullable (0).
+ * planes     [3] rows of n_tokens int32 at plane_stride: pos_offset + depth - amount, where depth is 0 without a parent
+ *            and the parent's + 1 with one.
+ * mask       [n_tokens][mask_words] uint64: bit b of word w of token i is set if token 64 w + b of its sequence is i
+ *            or an ancestor of it (tokens past 64 * mask_words have no bit).  mask_words 1..16.
+ * One launch.
+ * ------------------------------------------------------------------------------------------- */
+mrope_status mrope_planes_tree(const int32_t *parents, int64_t n_tokens, const int32_t *cu_seqlens, int32_t n_seqs,
+                               const int32_t *pos_offset, const int32_t *amount, int32_t *planes, int64_t plane_stride,
+                               uint64_t *mask, int32_t mask_words, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * mrope_attend_tree_kv8 -- mrope_attend_kv8 with a mask over the query tokens in the place of the causal one.
+ *
+ * Arguments, precision and workspace rules as in mrope_attend_kv8 (cu_seqlens is required); the positions that token
+ * i of len sees of a sequence of `context` are those before context - len, and context - len + j for every token j of
+ * the sequence whose bit is set in
+ * mask       [n_tokens][mask_words] uint64 (mrope_planes_tree's, or any other: a token need not see itself, or
+ *            may see later ones).  Tokens without a bit are not seen.  mask_words 1..64.
+ * ------------------------------------------------------------------------------------------- */
+size_t mrope_attend_tree_kv8_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                             int32_t head_dim, int32_t dtype, int32_t table_width, int32_t block_size);
+mrope_status mrope_attend_tree_kv8(const void *q, int64_t q_tok_stride, int64_t q_head_stride, int32_t n_q_heads,
+                                   int64_t n_tokens, int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                                   const int32_t *cu_seqlens, int32_t n_seqs, const int32_t *context_lens,
+                                   const uint64_t *mask, int32_t mask_words, const int32_t *block_tables,
+                                   int64_t table_stride, int32_t table_width, const void *k_cache, const void *v_cache,
+                                   const float *k_scale, const float *v_scale, int32_t block_size, int64_t num_blocks,
+                                   int64_t cache_block_stride, int64_t cache_tok_stride, int64_t cache_head_stride,
+                                   double softmax_scale, void *out, int64_t out_tok_stride, int64_t out_head_stride,
+                                   float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * mrope_verify_tree -- which drafted tokens the target accepts, and the token after them.
+ *
+ * target     [n_tokens] rows of `vocab` probabilities of `dtype` at target_stride (elements, >= vocab): the target's
+ *            distribution of the token that follows each token.  Entries that are not positive numbers count as 0.
+ *            Rows need no alignment but their elements'.
+ * draft      nullable, like target: the distribution that each token's children were drawn from, independently of
+ *            one another.  NULL: the children were not drawn (the drafter's best tokens, say).
+ * ids        [n_tokens] int32 (token 0's is not looked at; a draft outside [0, vocab) is passed over).
+ * parents    as above; NULL: chains, each token's parent is the one before it.
+ * u_accept [n_tokens], u_next [n_seqs] fp32 in [0, 1): the random numbers.
+ *
+ * From token 0 on: at token a, with r = target[a], c = 0 and Z = 1, its children are tested in their order.  Child x is
+ * accepted if u_accept[x] * q * Z < r(id_x), where q is draft[a](id_x), or 1 without draft; the walk goes on from it.
+ * If it is refused, c grows by Z, r becomes max(target[a] - c * draft[a], 0) and Z the sum of r; without draft r(id_x)
+ * becomes 0 and Z falls by what it was (not below 0).  Where no child is left, the next token is the smallest k with
+ * r(0) + .. + r(k) > u_next * (sum of r) and r(k) > 0 -- of target[a] itself if r has no mass, and -1 if that
+ * has none.  Drawn drafts are so accepted that the tokens are distributed as the target alone would draw them.
+ * All in 64 bits, in an order that does not change from call to call.
+ *
+ * n_kept     [n_seqs] int32 out: accepted tokens, token 0 included (0 for an empty tree).
+ * path       [n_tokens] int32 out: at cu_seqlens[s] + i the index of the i-th accepted token, -1 after the last.
+ * next_ids   [n_seqs] int32 out (-1 for an empty tree).
+ * workspace  256-byte aligned, mrope_verify_tree_workspace_bytes(...) bytes, needing no initialisation; calls that share
+ *            one must be ordered.
+ * ------------------------------------------------------------------------------------------- */
+size_t mrope_verify_tree_workspace_bytes(int32_t n_seqs, int32_t vocab, int32_t has_draft, int32_t has_parents);
+mrope_status mrope_verify_tree(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,
+                               int32_t vocab, int32_t dtype, int64_t n_tokens, const int32_t *ids, const int32_t *parents,
+                               const int32_t *cu_seqlens, int32_t n_seqs, const float *u_accept, const float *u_next,
+                               int32_t *n_kept, int32_t *path, int32_t *next_ids, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * mrope_keep_kv8 -- move the cache rows of accepted paths together, in the caches of every layer.
+ *
+ * layers     [n_layers] (host array): the caches and scales of each layer, all of one shape and strides.
+ * n_kept [n_seqs], path [n_tokens] int32: as mrope_verify_tree leaves them: of sequence s the i-th kept row is that of
+ *            token path[cu_seqlens[s] + i], i < n_kept[s].  The entries ascend; the first that does not, or lies
+ *            outside the tree, ends the list.
+ * pos_offset [n_seqs] int32: the position of each sequence's token 0 (negative: nothing is kept).
+ *
+ * The row at position pos_offset + path[i] goes to position pos_offset + i.  Each page that kept rows go to is
+ * left, for K and V and for each head, as an append of these rows' values (code * scale) at these positions would
+ * leave it (see above: the scale is that of the kept rows, and of the rows before pos_offset where it holds such): rows that stay
+ * may be re-coded too.  Rows that nothing is kept in stay as they are.  A row whose page is not there
+ * is not kept.  Pages that rows are kept in must not be shared with another sequence, as for an append.
+ * One launch.
+ * ------------------------------------------------------------------------------------------- */
+#define MROPE_MAX_LAYERS 64
+
+typedef struct {
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+} mrope_kv8_layer;
+
+mrope_status mrope_keep_kv8(const mrope_kv8_layer *layers, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
+                            int32_t block_size, int64_t num_blocks, int64_t cache_block_stride, int64_t cache_tok_stride,
+                            int64_t cache_head_stride, const int32_t *n_kept, const int32_t *path, int64_t n_tokens,
+                            const int32_t *cu_seqlens, int32_t n_seqs, const int32_t *pos_offset,
+                            const int32_t *block_tables, int64_t table_stride, int32_t table_width, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Pages of the paged caches: growing, freeing, forking, compacting, copying.
  *
  * The state, all on the device and owned by the caller:
