@@ -6,13 +6,17 @@
 // and ctx - len + b for the bits b that are set in its row of the mask.  Rows, tiles, chunks of contexts and the
 // join are those of mrope_attend.h; a row is a (token, head of the group) pair, row = i * g + head.
 //
-// One workgroup: 16, 32 or 64 rows against a chunk of the context, its four waves taking 32 tokens in turn, each
-// with all the rows.  S^T = K Q^T (16 x 16 x 32): a lane ends with the scores of one row of each sixteen (its
-// column) for eight neighbouring tokens, which is just the operand that O^T = V^T P^T wants of P, so nothing moves
-// between lanes and the waves meet only once, at the end.  A block's K and V are decoded once for all rows (codes
-// are exact in 16 bits, V with its scale).  The queries wait in LDS in the order of the instruction's operand.
-// P is taken in two bf16 terms for the 16-bit types and three for fp32, fp32 queries in three (each the bf16 nearest
-// to what the terms before it leave).
+// One workgroup: 32 or 64 rows against a chunk of the context, its four waves taking 32 tokens in turn, each
+// with all the rows.  S^T = K Q^T (32 x 32 x 16): a lane ends with the scores of one row of each thirty-two (its
+// column) for sixteen of the tokens, keys 8a + 4h + b, a, b < 4, of lane half h; O^T = V^T P^T takes sixteen tokens a step
+// and each lane's operand is what it has there, if V's comes in the same order.  So nothing moves between lanes
+// but for the maximum, and the waves meet only once, at the end.  A block's K and V are decoded once for all rows
+// (codes are exact in 16 bits, V with its scale).  P is taken in two bf16 terms for the 16-bit types and three for fp32,
+// fp32 queries in three (each the bf16 nearest to what the terms before it leave).
+//
+// Codes come to LDS by loads that pass no register, a block ahead, into a ring of the wave's own: no wave waits
+// for another.  The queries of 64 rows wait in LDS, in the order of the instruction's operand; those of 32 rows
+// stay in registers.
 //
 // Only blocks that reach past ctx - len, or into a page that is not there, look at the mask.
 #include <algorithm>
@@ -23,6 +27,7 @@ namespace mrope {
 namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTreeWaves = kFewWaves;
 template <int IO>
@@ -31,17 +36,17 @@ template <int IO>
 constexpr int kPTerms = IO == kIoF32 ? 3 : 2;
 
 template <int IO>
-__device__ __forceinline__ f32x4 mfma_scores(u32x4 x, u32x4 y, f32x4 c)
+__device__ __forceinline__ f32x16 mfma_scores(u32x4 x, u32x4 y, f32x16 c)
 {
     if constexpr (IO == kIoF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
     else
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ f32x4 mfma_bf16(u32x4 x, u32x4 y, f32x4 c)
+__device__ __forceinline__ f32x16 mfma_bf16(u32x4 x, u32x4 y, f32x16 c)
 {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
 }
 
 // Two e4m3 bytes of a key as the scores' 16-bit type (exact).  bf16 takes the page's scale at once; fp16 has no
@@ -53,34 +58,113 @@ __device__ __forceinline__ uint32_t key_pair(uint32_t u, float scale)
     else return bf16_pair<HI>(u, scale);
 }
 
-template <int IO, int D, int NB>
-struct alignas(16) TreeLds {
-    union {
-        u32x4 q[NB][kQTerms<IO>][D / 32][64];  // the operand's pieces by lane
-        float o[kTreeWaves][16][D + 4];        // sixteen rows' parts, when the queries have done their work
-    };
-    float ml[kTreeWaves][16 * NB][2];
+// Codes of 32 tokens on their way, as they lie in the cache but for the order of a row's 16-byte pieces (K) and of the
+// rows (V): so chosen that the lanes of a read lie in different banks.
+template <int D>
+struct alignas(16) Block {
+    uint8_t k[32 * D], v[32 * D];
 };
 
-// Workgroups of a compute unit that the registers let run at once.
-constexpr int tree_resident(int head_dim, int nb)
+template <int IO, int D, int NB>
+struct alignas(16) TreeLds {
+    static constexpr bool kQueries = NB > 1;  // the queries are here
+    union {
+        struct {
+            Block<D> ring[kTreeWaves][2];                        // of each wave: this block and the next
+            u32x4 q[kQueries ? NB : 0][kQTerms<IO>][D / 16][64];  // the operand's pieces by lane
+        };
+        struct {                                                 // when the last block is done
+            float o[kTreeWaves][32][D + 4];                      // thirty-two rows' parts
+            float ml[kTreeWaves][32 * NB][2];
+        };
+    };
+};
+
+// 16 bytes a lane from global memory (g, the same in all lanes, and an offset) to LDS, where the lanes' lie one after
+// the other from `l` on.
+__device__ __forceinline__ void to_lds16(const uint8_t *g, uint32_t off, uint8_t *l)
 {
-    const int r = head_dim * nb;
-    return r >= 512 ? 1 : (r >= 256 ? 2 : (r >= 128 ? 3 : 4));
+    typedef const __attribute__((address_space(1))) uint8_t *Global;
+    __builtin_amdgcn_global_load_lds((Global)g + off, (__attribute__((address_space(3))) void *)l, 16, 0, 0);
+}
+
+// Where row r of 32 has its 16-byte piece p of K, and its row of V.
+template <int D>
+__device__ __forceinline__ int key_piece_of(int r, int p)
+{
+    if constexpr (D == 256) return p ^ (r & 15);
+    else if constexpr (D == 128) return p ^ ((r >> 1) & 7);
+    else return p ^ ((r >> 2) & 3);
+}
+template <int D>
+__device__ __forceinline__ int value_row_of(int r)
+{
+    return D == 256 ? r : r ^ ((r >> 2) & 1);
+}
+
+// The bytes of V that a lane holds of a token: D / 32 dims.
+template <int D>
+struct VPiece {
+    uint32_t w[D == 256 ? 2 : 1];
+};
+template <int D>
+__device__ __forceinline__ VPiece<D> load_vpiece(const uint8_t *p)
+{
+    VPiece<D> r;
+    if constexpr (D == 256) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        r.w[0] = x.x, r.w[1] = x.y;
+    } else if constexpr (D == 128) {
+        r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
+        r.w[0] = *reinterpret_cast<const uint16_t *>(p);
+    }
+    return r;
+}
+
+// Workgroups of a compute unit that LDS and the registers let run at once.
+constexpr int tree_resident(int io, int head_dim, int nb)
+{
+    if (head_dim == 256 || (io == kIoF32 && head_dim == 128)) return 1;
+    if (head_dim == 128 || nb > 1 || io == kIoF32) return 2;
+    return 3;
+}
+
+// The output's sums stay where they are: with one workgroup a compute unit in the accumulation registers.
+template <int IO, int D, int NB>
+__device__ __forceinline__ void pin(f32x16 &x)
+{
+    if constexpr (tree_resident(IO, D, NB) == 1) asm volatile("" : "+a"(x));
+    else asm volatile("" : "+v"(x));
+}
+
+// The largest of three (of the others where one is NaN), without the canonicalisation that fmaxf costs.
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    return r;
+}
+
+// The larger of a lane's and its counterpart's in the other half of the wave.
+__device__ __forceinline__ float max_halves(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return max3(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[1]));
 }
 
 // V's page scale (2^8 smaller) beside which the running maximum follows at once.
 constexpr float kLargeScale = 0x1p72f;
 
 template <int IO, int D, int NB>
-__global__ __launch_bounds__(64 * kTreeWaves, tree_resident(D, NB)) void attend_tree_kernel(AttendTree a, FewPlan p)
+__global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void attend_tree_kernel(AttendTree a, FewPlan p)
 {
-    constexpr int R = 16 * NB, QT = kQTerms<IO>, N = kPTerms<IO>;
-    constexpr int NK = D / 64;   // 16-byte pieces of a key a lane holds
-    constexpr int ND = D / 16;   // dims a lane's V operand holds of a token, and 16-dim tiles of O^T
+    constexpr int R = 32 * NB, QT = kQTerms<IO>, N = kPTerms<IO>;
+    constexpr int NS = D / 16;   // steps of a score
+    constexpr int NO = D / 32;   // dims of V that a lane holds of a token, and 32-dim tiles of O^T
     const Kv8 &kv = a.kv;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int col = lane & 15, grp = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int col = lane & 31, half = lane >> 5;
     const int g = a.nq / kv.nk, kvh = blockIdx.y;
 
     Cut cut = {0, 0, 0, 1};
@@ -102,268 +186,297 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(D, NB)) void attend_
     }
     const int n_rows = min(R, tl.rows - tl.row0);
     const int32_t len = tl.rows / g;
-    const int32_t seen = (int32_t)tl.seen, past = (int32_t)tl.past;  // (past >= -2^31: ctx >= 0)
+    const int32_t seen = __builtin_amdgcn_readfirstlane((int32_t)tl.seen);
+    const int32_t past = __builtin_amdgcn_readfirstlane((int32_t)tl.past);  // (>= -2^31: ctx >= 0)
     const int32_t open = min(max(past, 0), seen);                     // every row sees the positions before this
     const int32_t chunk = chunk_of(seen, cut.n, kFewUnit);
-    const int32_t c0 = (int32_t)min((int64_t)z * chunk, (int64_t)seen), c1 = min(c0 + chunk, seen);
+    const int32_t c0 = __builtin_amdgcn_readfirstlane((int32_t)min((int64_t)z * chunk, (int64_t)seen));
+    const int32_t c1 = __builtin_amdgcn_readfirstlane(min(c0 + chunk, seen));
 
     __shared__ TreeLds<IO, D, NB> lds;
 
-    // pages of this wave's half blocks from token `from` on, a lane each
+    // Blocks of 32 tokens: this wave's i-th begins at c0 + (4 i + wave) * 32.  Pages of 32 of them at a time, those of a
+    // sixteen of tokens a lane.
     const int32_t *table = kv.tables + tl.s * kv.table_stride;
     int64_t base;
-    float ks, vs;
+    float ks_lane, vs_lane;
     uint64_t valid_mask;
-    auto look_up = [&](int32_t from) {
+    auto look_up = [&](int i) {
         base = 0;
-        ks = vs = 1.0f;
+        ks_lane = vs_lane = 1.0f;
         bool valid = false;
-        const int64_t tok = (int64_t)from + ((lane >> 1) * kTreeWaves + wave) * 32 + (lane & 1) * 16;
+        const int64_t tok = (int64_t)c0 + ((i + (lane >> 1)) * kTreeWaves + wave) * 32 + (lane & 1) * 16;
         if (tok < c1) {
             const int32_t page = table[tok >> kv.bs_shift];
             valid = page >= 0 && page < kv.num_blocks;
             if (valid) {
-                ks = kv.k_scale[(int64_t)page * kv.nk + kvh];
-                vs = pow2(scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]) - kVDown);  // (finite, whatever nobody sees)
+                ks_lane = kv.k_scale[(int64_t)page * kv.nk + kvh];
+                vs_lane = pow2(scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]) - kVDown);  // (finite, whatever nobody sees)
                 base = page * kv.c_block;
             }
             base += (tok & (kv.block_size - 1)) * kv.c_tok + kvh * kv.c_head;
         }
         valid_mask = __ballot(valid);
     };
-    auto blocks_of = [&](int32_t from) {  // of this wave, in the tokens looked up from there
-        const int n = (min(c1 - from, kFewPages) + 31) / 32;
-        return n > wave ? (n - wave + kTreeWaves - 1) / kTreeWaves : 0;
+    struct Info {  // of a block: scales and whether the page is there, by sixteens of tokens
+        float ks0, ks1, vs0, vs1;
+        bool ok0, ok1;
     };
-    look_up(c0);
-
-    u32x4 ka[NK], kb[NK];
-    VRow<D> vr[8];
-    const int key = (col >> 2) * 8 + (col & 3);  // the tiles' keys: this one, and four further
-    auto half_base = [&](int i, int half) {
-        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)base, 2 * i + half);
-        const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)base >> 32), 2 * i + half);
-        return (int64_t)(((uint64_t)hi << 32) | lo);
-    };
-    auto load_k = [&](int i) {
-        const int64_t b0 = half_base(i, 0), b1 = half_base(i, 1);
-        const uint8_t *p = kv.k + (col < 8 ? b0 : b1) + (key & 15) * kv.c_tok + grp * 16;
+    Info next;
+    Block<D> *ring = lds.ring[wave];
+    // An instruction brings 1 KB: RI rows, and the lanes' places within them.
+    constexpr int RI = 1024 / D, NI = 32 / RI, PR = D / 16;
+    constexpr int KV = 16 / RI < NI ? 16 / RI : NI;  // places that differ: K's order of pieces goes by a row of sixteen
+    uint32_t koff[KV], voff[2];
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            ka[k] = *reinterpret_cast<const u32x4 *>(p + 64 * k);
-            kb[k] = *reinterpret_cast<const u32x4 *>(p + 4 * kv.c_tok + 64 * k);
+    for (int i = 0; i < KV; ++i) koff[i] = (lane / PR) * (uint32_t)kv.c_tok + 16 * key_piece_of<D>(i * RI + lane / PR, lane % PR);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) voff[i] = (value_row_of<D>(i * RI + lane / PR) - i * RI) * (uint32_t)kv.c_tok + 16 * (lane % PR);
+    auto fetch = [&](int i) {  // block i, on its way to the ring
+        if (i && (i & 31) == 0) look_up(i);
+        const int at = 2 * (i & 31);
+        next.ks0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks_lane), at));
+        next.ks1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks_lane), at + 1));
+        next.vs0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs_lane), at));
+        next.vs1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs_lane), at + 1));
+        next.ok0 = (valid_mask >> at) & 1, next.ok1 = (valid_mask >> (at + 1)) & 1;
+        Block<D> &to = ring[i & 1];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)base, at + half);
+            const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)base >> 32), at + half);
+            const int64_t b = (int64_t)(((uint64_t)hi << 32) | lo);
+#pragma unroll
+            for (int j = half * NI / 2; j < (half + 1) * NI / 2; ++j)
+                to_lds16(kv.k + (b + (j * RI) % 16 * kv.c_tok), koff[j % KV], to.k + 1024 * j);
+#pragma unroll
+            for (int j = half * NI / 2; j < (half + 1) * NI / 2; ++j)
+                to_lds16(kv.v + (b + (j * RI) % 16 * kv.c_tok), voff[j & 1], to.v + 1024 * j);
         }
     };
-    auto load_v = [&](int i) {
-        const int64_t b0 = half_base(i, 0), b1 = half_base(i, 1);
-        const uint8_t *p = kv.v + (grp < 2 ? b0 : b1) + (grp & 1) * 8 * kv.c_tok + col * ND;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) vr[j] = load_vrow<D>(p + j * kv.c_tok);
-    };
-    int n_mine = blocks_of(c0);
+    const int n_all = (c1 - c0 + 31) / 32, n_mine = n_all > wave ? (n_all - wave + kTreeWaves - 1) / kTreeWaves : 0;
     if (n_mine > 0) {
-        load_k(0);
-        load_v(0);
+        look_up(0);
+        fetch(0);
     }
 
-    // the queries: piece f of lane (col, grp) is dims 64 * (f / 2) + 16 * grp + 8 * (f % 2) .. + 7 of row col
-    for (int e = threadIdx.x; e < NB * (D / 32) * 64; e += 64 * kTreeWaves) {
-        const int el = e & 63, f = (e >> 6) % (D / 32), nb = (e >> 6) / (D / 32);
-        const int r = nb * 16 + (el & 15);
+    // the scores' factor: its sign goes to Q, and zero makes Q zero, so the largest score is the largest sum
+    const float factor = a.scale_log2 != 0.0f ? __builtin_fabsf(a.scale_log2) : 1.0f;
+    const float sign = a.scale_log2 < 0.0f ? -1.0f : (a.scale_log2 > 0.0f ? 1.0f : 0.0f);
+
+    // The queries: piece s of lane (col, half) is dims 32 * (s / 2) + 16 * half + 8 * (s % 2) .. + 7 of row col.
+    auto query_terms = [&](int r, int s, int h, u32x4 (&w)[QT]) {
         float x[8] = {};
         if (r < n_rows) {
             const int row = tl.row0 + r;
             unpack8<IO>(load8<IO>(a.q, (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head +
-                                           64 * (f >> 1) + 16 * (el >> 4) + 8 * (f & 1)), x);
+                                           32 * (s >> 1) + 16 * h + 8 * (s & 1)), x);
         }
 #pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            u32x4 w;
+        for (int i = 0; i < 8; ++i) x[i] *= sign;
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                w[i] = pack16x2<IO == kIoF16 ? kIoF16 : kIoBF16>(x[2 * i], x[2 * i + 1]);
+                w[t][i] = pack16x2<IO == kIoF16 ? kIoF16 : kIoBF16>(x[2 * i], x[2 * i + 1]);
                 if (t + 1 < QT) {
                     float lo, hi;
-                    unpack16x2<kIoBF16>(w[i], lo, hi);
+                    unpack16x2<kIoBF16>(w[t][i], lo, hi);
                     x[2 * i] -= lo;
                     x[2 * i + 1] -= hi;
                 }
             }
-            lds.q[nb][t][f][el] = w;
-        }
-    }
-    __syncthreads();
-
-    int32_t itok[NB];  // the query token of this lane's row of each sixteen
+    };
+    constexpr bool kQueries = TreeLds<IO, D, NB>::kQueries;
+    u32x4 qreg[kQueries ? 1 : NS][QT];
+    if constexpr (kQueries) {
+        for (int e = threadIdx.x; e < NB * NS * 64; e += 64 * kTreeWaves) {
+            const int el = e & 63, s = (e >> 6) % NS, nb = (e >> 6) / NS;
+            u32x4 w[QT];
+            query_terms(nb * 32 + (el & 31), s, el >> 5, w);
 #pragma unroll
-    for (int n = 0; n < NB; ++n) itok[n] = (tl.row0 + min(n * 16 + col, n_rows - 1)) / g;
-    // Which of the tokens mine0 .. + 7 query token i sees: bit q for mine0 + q.
-    auto sees = [&](int32_t i, int32_t mine0, bool ok) {
-        const int32_t j = mine0 - past;  // (the tree's token at mine0)
+            for (int t = 0; t < QT; ++t) lds.q[nb][t][s][el] = w[t];
+        }
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) query_terms(col, s, half, qreg[s]);
+    }
+
+    int32_t itok[NB];  // the query token of this lane's row of each thirty-two
+#pragma unroll
+    for (int n = 0; n < NB; ++n) itok[n] = (tl.row0 + min(n * 32 + col, n_rows - 1)) / g;
+    // Which of the tokens tok0 .. + 31 query token i sees: bit q for tok0 + q.
+    auto sees = [&](int32_t i, int32_t tok0, bool ok0, bool ok1) {
+        const int32_t j = tok0 - past;  // (the tree's token at tok0)
         const uint64_t *row = a.mask + (int64_t)(tl.t0 + i) * a.mask_words;
         const int32_t w = j >> 6;
         auto word = [&](int32_t k) { return k < 0 ? ~0ull : (k < a.mask_words ? row[k] : 0ull); };
         uint64_t bits = word(w) >> (j & 63);
-        if ((j & 63) > 56) bits |= word(w + 1) << (64 - (j & 63));
-        const int32_t n = min(min(len - j, seen - mine0), 8);
-        return n > 0 && ok ? (uint32_t)bits & ((1u << n) - 1) : 0u;
+        if ((j & 63) > 32) bits |= word(w + 1) << (64 - (j & 63));
+        const int32_t n = min(min(len - j, seen - tok0), 32);
+        const uint32_t there = (ok0 ? 0xffffu : 0u) | (ok1 ? 0xffff0000u : 0u);
+        return n > 0 ? (uint32_t)bits & (0xffffffffu >> (32 - n)) & there : 0u;
     };
 
     float m[NB], l[NB];
-    f32x4 o[NB][ND];
+    f32x16 o[NB][NO];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         m[n] = kNoMax;
         l[n] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < ND; ++i) o[n][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < NO; ++i) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[n][i][q] = 0.0f;
+            pin<IO, D, NB>(o[n][i]);
+        }
     }
 
-    for (int32_t from = c0;;) {
-        for (int it = 0; it < n_mine; ++it) {
-            const int32_t tok0 = from + (it * kTreeWaves + wave) * 32;
-            const float ks0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks), 2 * it));
-            const float ks1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks), 2 * it + 1));
-            const float kscale = col < 8 ? ks0 : ks1;
-            const bool ok0 = (valid_mask >> (2 * it)) & 1, ok1 = (valid_mask >> (2 * it + 1)) & 1;
-            int here = lane;  // (opaque: the queries stay in LDS and are read anew)
-            asm volatile("" : "+v"(here));
-            f32x4 sa[NB], sb[NB];
-#pragma unroll
-            for (int n = 0; n < NB; ++n) sa[n] = sb[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < NK; ++k)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const u32x4 fa = {key_pair<IO, false>(ka[k][2 * h], kscale), key_pair<IO, true>(ka[k][2 * h], kscale),
-                                      key_pair<IO, false>(ka[k][2 * h + 1], kscale), key_pair<IO, true>(ka[k][2 * h + 1], kscale)};
-                    const u32x4 fb = {key_pair<IO, false>(kb[k][2 * h], kscale), key_pair<IO, true>(kb[k][2 * h], kscale),
-                                      key_pair<IO, false>(kb[k][2 * h + 1], kscale), key_pair<IO, true>(kb[k][2 * h + 1], kscale)};
-#pragma unroll
-                    for (int t = 0; t < QT; ++t)
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) {
-                            const u32x4 q = lds.q[n][t][2 * k + h][here];
-                            sa[n] = mfma_scores<IO>(fa, q, sa[n]);
-                            sb[n] = mfma_scores<IO>(fb, q, sb[n]);
-                        }
-                }
-            if (it + 1 < n_mine) load_k(it + 1);
+    uint32_t nan = 0;  // a block with a mask had one in V
+    for (int it = 0; it < n_mine; ++it) {
+        const int32_t tok0 = c0 + (it * kTreeWaves + wave) * 32;
+        // this block has come, and what was read of the one before it is there
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        const Info now = next;
+        const Block<D> &blk = ring[it & 1];
+        if (it + 1 < n_mine) fetch(it + 1);
+        const float kscale = col < 16 ? now.ks0 : now.ks1;
+        int here = lane;  // (opaque: the queries stay in LDS and are read anew)
+        asm volatile("" : "+v"(here));
 
-            // this lane: a row of each sixteen against tokens tok0 + 8*grp + 0..7
-            const float vs0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs), 2 * it));
-            const float vs1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs), 2 * it + 1));
-            const float vscale = grp < 2 ? vs0 : vs1;
-            const bool edge = tok0 + 32 > open || !ok0 || !ok1;  // wave-uniform
-            const int32_t mine0 = tok0 + 8 * grp;
-            // the maximum moves only where it has grown by 2^8: until then p exceeds 1 and nothing is lost (but
-            // beside large values, where the sums have no room for it, it moves at once)
-            const float lag = fmaxf(vs0, vs1) >= kLargeScale ? 0.0f : 8.0f;
-            uint32_t vis[NB];
-            u32x4 pf[NB][N];
+        // The scores, step by step, their operands read kAhead steps before their use.
+        constexpr int kSteps = kQueries ? NS * NB : 0, kAhead = kQueries ? 6 : 1;
+        u32x4 kp[NS / 2], q[kAhead];
+        auto query = [&](int i) { return lds.q[i % NB][0][i / NB][here]; };
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                float p[8];
+        for (int k = 0; k < NS / 2; ++k) {
+            kp[k] = *reinterpret_cast<const u32x4 *>(blk.k + col * D + 16 * key_piece_of<D>(col, 2 * k + half));
+            if constexpr (kQueries) {
+                if (k == 0) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    p[j] = sa[n][j];
-                    p[4 + j] = sb[n][j];
+                    for (int i = 0; i < kAhead; ++i)
+                        if (i < kSteps) q[i] = query(i);
                 }
-                if constexpr (IO == kIoF16) {
-                    const float f = grp < 2 ? ks0 : ks1;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) p[j] *= f;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] *= a.scale_log2;
-                vis[n] = 0xff;
-                if (edge) {
-                    vis[n] = sees(itok[n], mine0, grp < 2 ? ok0 : ok1);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (!(vis[n] >> j & 1)) p[j] = -__builtin_inff();
-                }
-                float mx = p[0];
-#pragma unroll
-                for (int j = 1; j < 8; ++j) mx = fmaxf(mx, p[j]);
-                mx = fmaxf(mx, __shfl_xor(mx, 16));
-                mx = fmaxf(mx, __shfl_xor(mx, 32));
-                if (__any(mx > m[n] + lag)) {
-                    const float m_new = fmaxf(m[n], mx);
-                    const float f = __builtin_amdgcn_exp2f(m[n] - m_new);
-                    l[n] *= f;
-#pragma unroll
-                    for (int i = 0; i < ND; ++i) o[n][i] *= f;
-                    m[n] = m_new;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    p[j] = __builtin_amdgcn_exp2f(p[j] - m[n]);
-                    l[n] += p[j];
-                }
-#pragma unroll
-                for (int t = 0; t < N; ++t)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t w = pack16x2<kIoBF16>(p[2 * j], p[2 * j + 1]);
-                        pf[n][t][j] = w;
-                        if (t + 1 < N) {
-                            float lo, hi;
-                            unpack16x2<kIoBF16>(w, lo, hi);
-                            p[2 * j] -= lo;
-                            p[2 * j + 1] -= hi;
-                        }
-                    }
             }
+        }
+        f32x16 s[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[n][e] = 0.0f;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            const int h = k & 1;
+            const u32x4 f = {key_pair<IO, false>(kp[k >> 1][2 * h], kscale), key_pair<IO, true>(kp[k >> 1][2 * h], kscale),
+                             key_pair<IO, false>(kp[k >> 1][2 * h + 1], kscale), key_pair<IO, true>(kp[k >> 1][2 * h + 1], kscale)};
+            if constexpr (kQueries) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const int i = k * NB + n;
+                    s[n] = mfma_scores<IO>(f, q[i % kAhead], s[n]);
+                    if (i + kAhead < kSteps) q[i % kAhead] = query(i + kAhead);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            } else {
+#pragma unroll
+                for (int t = 0; t < QT; ++t) s[0] = mfma_scores<IO>(f, qreg[k][t], s[0]);
+            }
+        }
+        // V's bytes: step u of sixteen tokens, tokens 16 u + 8 a + 4 half + b
+        VPiece<D> vp[2][8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                vp[u][j] = load_vpiece<D>(blk.v + value_row_of<D>(16 * u + 8 * (j >> 2) + 4 * half + (j & 3)) * D + col * NO);
+        __builtin_amdgcn_sched_barrier(0);
 
-            // A NaN that some rows see and others do not, or that nobody sees, must not reach the product: there it
-            // is left out, and the rows that see it are told.
-            bool nan = false;
+        const bool edge = tok0 + 32 > open || !now.ok0 || !now.ok1;  // wave-uniform
+        // (fp16: not 0, which would make a masked -infinity NaN, nor past fp32)
+        const float f0 = IO == kIoF16 ? fminf(fmaxf(now.ks0 * factor, 0x1p-126f), 0x1p127f) : factor;
+        const float f1 = IO == kIoF16 ? fminf(fmaxf(now.ks1 * factor, 0x1p-126f), 0x1p127f) : factor;
+        // the maximum moves only where it has grown by 2^8: until then p exceeds 1 and nothing is lost (but
+        // beside large values, where the sums have no room for it, it moves at once)
+        const float lag = fmaxf(now.vs0, now.vs1) >= kLargeScale ? 0.0f : 8.0f;
+        u32x4 pf[NB][2][N];  // P's terms by step
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
             if (edge) {
+                const uint32_t vis = sees(itok[n], tok0, now.ok0, now.ok1) >> (4 * half);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (!(vis >> (8 * (e >> 2) + (e & 3)) & 1)) s[n][e] = -__builtin_inff();
+            }
+            auto top8 = [&](int e) {
+                return max3(max3(s[n][e], s[n][e + 1], s[n][e + 2]), max3(s[n][e + 3], s[n][e + 4], s[n][e + 5]), max3(s[n][e + 6], s[n][e + 7], s[n][e + 7]));
+            };
+            const float t0 = top8(0) * f0, t1 = top8(8) * f1;
+            const float top = max_halves(max3(t0, t1, t1));
+            if (__any(top > m[n] + lag)) {
+                const float m_new = fmaxf(m[n], top);
+                const float c = __builtin_amdgcn_exp2f(m[n] - m_new);
+                l[n] *= c;
+#pragma unroll
+                for (int i = 0; i < NO; ++i) {
+                    pin<IO, D, NB>(o[n][i]);
+                    o[n][i] *= c;
+                    pin<IO, D, NB>(o[n][i]);
+                }
+                m[n] = m_new;
+            }
+            float add[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e], e < 8 ? f0 : f1, -m[n]));
+                float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e + 1], e < 8 ? f0 : f1, -m[n]));
+                add[0] += p0;
+                add[1] += p1;
+#pragma unroll
+                for (int t = 0; t < N; ++t) {
+                    const uint32_t w = pack16x2<kIoBF16>(p0, p1);
+                    pf[n][e >> 3][t][(e & 7) >> 1] = w;
+                    if (t + 1 < N) {
+                        float lo, hi;
+                        unpack16x2<kIoBF16>(w, lo, hi);
+                        p0 -= lo;
+                        p1 -= hi;
+                    }
+                }
+            }
+            l[n] += add[0] + add[1];
+        }
+
+        // A NaN that some rows see and others do not, or that nobody sees, must not reach the product: the product
+        // goes on without it, and the rows that see it are told at the end.
+        if (edge) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
-                    for (int w = 0; w < ND / 4; ++w) nan |= any_nan(vr[j].w[w]);
-                nan = __any(nan);
-            }
+                    for (int w = 0; w < (D == 256 ? 2 : 1); ++w) {
+                        uint32_t &x = vp[u][j].w[w];
+                        const uint32_t bad = (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in a NaN's byte
+                        nan |= bad;
+                        x &= ~(bad * 0xffu);
+                    }
+        }
 #pragma unroll
-            for (int w = 0; w < ND / 4; ++w) {
-                // bytes of two tokens side by side, then bf16 pairs (token 2j, token 2j + 1) of one dim
+        for (int u = 0; u < 2; ++u) {
+            const float vscale = u ? now.vs1 : now.vs0;
+#pragma unroll
+            for (int w = 0; w < (NO + 3) / 4; ++w) {
+                // bytes of two tokens side by side, then bf16 pairs (token, next token) of one dim
                 uint32_t lo[4], hi[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    lo[j] = __builtin_amdgcn_perm(vr[2 * j + 1].w[w], vr[2 * j].w[w], 0x05010400u);
-                    hi[j] = __builtin_amdgcn_perm(vr[2 * j + 1].w[w], vr[2 * j].w[w], 0x07030602u);
-                }
-                if (nan) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        u32x4 ind;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t &b = e < 2 ? lo[j] : hi[j];
-                            const int sh = (e & 1) * 16;
-                            const uint32_t x = b >> sh;
-                            const bool n0 = (x & 0x7fu) == 0x7fu, n1 = (x & 0x7f00u) == 0x7f00u;
-                            ind[j] = (n0 ? 0x3f80u : 0u) | (n1 ? 0x3f800000u : 0u);
-                            if (n0) b &= ~(0xffu << sh);
-                            if (n1) b &= ~(0xff00u << sh);
-                        }
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) {
-                            u32x4 mine;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                mine[j] = (vis[n] >> (2 * j) & 1 ? 0x3f80u : 0u) | (vis[n] >> (2 * j + 1) & 1 ? 0x3f800000u : 0u);
-                            const f32x4 cnt = mfma_bf16(ind, mine, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (cnt[q] > 0.0f) o[n][4 * w + e][q] = __builtin_nanf("");
-                        }
-                    }
+                    lo[j] = __builtin_amdgcn_perm(vp[u][2 * j + 1].w[w], vp[u][2 * j].w[w], 0x05010400u);
+                    if (NO > 2) hi[j] = __builtin_amdgcn_perm(vp[u][2 * j + 1].w[w], vp[u][2 * j].w[w], 0x07030602u);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < (NO < 4 ? NO : 4); ++e) {
                     u32x4 fv;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -373,29 +486,71 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(D, NB)) void attend_
 #pragma unroll
                     for (int t = 0; t < N; ++t)
 #pragma unroll
-                        for (int n = 0; n < NB; ++n) o[n][4 * w + e] = mfma_bf16(fv, pf[n][t], o[n][4 * w + e]);
+                        for (int n = 0; n < NB; ++n) o[n][4 * w + e] = mfma_bf16(fv, pf[n][u][t], o[n][4 * w + e]);
                 }
             }
-            if (it + 1 < n_mine) load_v(it + 1);
         }
-        if (c1 - from <= kFewPages) break;
-        from += kFewPages;
-        look_up(from);
-        n_mine = blocks_of(from);
-        if (n_mine > 0) {
-            load_k(0);
-            load_v(0);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < NO; ++i) pin<IO, D, NB>(o[n][i]);
+    }
+
+    if (__any(nan != 0)) {  // (rare) the blocks with a mask again: the rows that see a NaN have it in these dims
+#pragma unroll 1
+        for (int it = 0; it < n_mine; ++it) {
+            const int32_t tok0 = c0 + (it * kTreeWaves + wave) * 32;
+            if ((it & 31) == 0) look_up(it);
+            const int at = 2 * (it & 31);
+            const bool ok0 = (valid_mask >> at) & 1, ok1 = (valid_mask >> (at + 1)) & 1;
+            if (tok0 + 32 <= open && ok0 && ok1) continue;
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)base, at + u);
+                const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)base >> 32), at + u);
+                const int64_t b = (int64_t)(((uint64_t)hi << 32) | lo);
+                VPiece<D> vp[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) vp[j] = load_vpiece<D>(kv.v + b + (8 * (j >> 2) + 4 * half + (j & 3)) * kv.c_tok + col * NO);
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const uint32_t vis = sees(itok[n], tok0, ok0, ok1) >> (16 * u + 4 * half);
+                    u32x4 mine;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mine[j] = (vis >> (8 * (j >> 1) + 2 * (j & 1)) & 1 ? 0x3f80u : 0u) | (vis >> (8 * (j >> 1) + 2 * (j & 1) + 1) & 1 ? 0x3f800000u : 0u);
+#pragma unroll
+                    for (int i = 0; i < NO; ++i) {
+                        u32x4 ind;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t x = vp[2 * j].w[i / 4] >> (8 * (i % 4)), y = vp[2 * j + 1].w[i / 4] >> (8 * (i % 4));
+                            ind[j] = ((x & 0x7f) == 0x7f ? 0x3f80u : 0u) | ((y & 0x7f) == 0x7f ? 0x3f800000u : 0u);
+                        }
+                        f32x16 cnt;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) cnt[e] = 0.0f;
+                        cnt = mfma_bf16(ind, mine, cnt);
+                        pin<IO, D, NB>(o[n][i]);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (cnt[e] > 0.0f) o[n][i][e] = __builtin_nanf("");
+                        pin<IO, D, NB>(o[n][i]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
         }
     }
 
-    // the waves' parts meet in LDS, sixteen rows at a time
+    // the waves' parts meet in LDS, thirty-two rows at a time
+    __syncthreads();  // (the ring and the queries have been read)
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-        l[n] += __shfl_xor(l[n], 16);
         l[n] += __shfl_xor(l[n], 32);
-        if (lane < 16) {
-            lds.ml[wave][n * 16 + col][0] = m[n];
-            lds.ml[wave][n * 16 + col][1] = l[n];
+        if (half == 0) {
+            lds.ml[wave][n * 32 + col][0] = m[n];
+            lds.ml[wave][n * 32 + col][1] = l[n];
         }
     }
     const bool whole = cut.n == 1;
@@ -403,18 +558,22 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(D, NB)) void attend_
                           ((int64_t)(cut.slot + z) * kv.nk + kvh);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-        if (n * 16 >= n_rows) break;
-        __syncthreads();  // the queries, or the sixteen rows before, have been read
+        if (n * 32 >= n_rows) break;
+        if (n) __syncthreads();  // the rows before have been read
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float *dst = &lds.o[wave][col][(grp * 4 + q) * ND];
+        for (int e = 0; e < 16; ++e) {
+            float *dst = &lds.o[wave][col][(8 * (e >> 2) + 4 * half + (e & 3)) * NO];
+            if constexpr (NO >= 4) {
 #pragma unroll
-            for (int i = 0; i < ND; i += 4)
-                *reinterpret_cast<f32x4 *>(dst + i) = f32x4{o[n][i][q], o[n][i + 1][q], o[n][i + 2][q], o[n][i + 3][q]};
+                for (int i = 0; i < NO; i += 4) *reinterpret_cast<f32x4 *>(dst + i) = f32x4{o[n][i][e], o[n][i + 1][e], o[n][i + 2][e], o[n][i + 3][e]};
+            } else {
+#pragma unroll
+                for (int i = 0; i < NO; ++i) dst[i] = o[n][i][e];
+            }
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < min(16, n_rows - n * 16) * (D / 8); e += 64 * kTreeWaves) {
-            const int r16 = e / (D / 8), rr = n * 16 + r16, d = e % (D / 8) * 8;
+        for (int e = threadIdx.x; e < min(32, n_rows - n * 32) * (D / 8); e += 64 * kTreeWaves) {
+            const int r32 = e / (D / 8), rr = n * 32 + r32, d = e % (D / 8) * 8;
             float mm = kNoMax, ll = 0.0f, y[8] = {};
 #pragma unroll
             for (int w = 0; w < kTreeWaves; ++w) mm = fmaxf(mm, lds.ml[w][rr][0]);
@@ -423,7 +582,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(D, NB)) void attend_
                 const float f = __builtin_amdgcn_exp2f(lds.ml[w][rr][0] - mm);
                 ll += lds.ml[w][rr][1] * f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] += lds.o[w][r16][d + i] * f;
+                for (int i = 0; i < 8; ++i) y[i] += lds.o[w][r32][d + i] * f;
             }
             if (whole) {
                 const int rw = tl.row0 + rr;
@@ -449,21 +608,22 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(D, NB)) void attend_
 
 // ------------------------------------------------------------------ launchers ------------------
 struct TreePlan {
-    int nb;         // sixteens of rows of a tile
+    int nb;         // thirty-twos of rows of a tile
     int64_t tiles, grid;
     FewPlan few;
     size_t bytes;   // of the workspace
 };
 
-TreePlan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int32_t table_width, int32_t block_size)
+TreePlan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io, int32_t table_width,
+                   int32_t block_size)
 {
     TreePlan p{};
     const int64_t g = nq / nk, cap = std::max<int64_t>(1, (int64_t)table_width * block_size);
     const int64_t seq_rows = (n_tokens * g + n_seqs - 1) / n_seqs;
-    p.nb = seq_rows <= 16 ? 1 : (seq_rows <= 32 || head_dim == 256 ? 2 : 4);
-    const int64_t rows = 16 * p.nb, most = (cap + kFewUnit - 1) / kFewUnit;
+    p.nb = seq_rows <= 32 || io == kIoF32 ? 1 : 2;
+    const int64_t rows = 32 * p.nb, most = (cap + kFewUnit - 1) / kFewUnit;
     p.tiles = n_tokens * g / rows + n_seqs;
-    p.few.budget = std::max(1, 256 * tree_resident(head_dim, p.nb) / nk);
+    p.few.budget = std::max(1, 256 * tree_resident(io, head_dim, p.nb) / nk);
     p.grid = std::min(p.tiles + p.few.budget, p.tiles * most);
     if (most > 1) {
         p.few.max_cut = (int32_t)std::min<int64_t>(p.tiles, p.few.budget);
@@ -476,7 +636,7 @@ TreePlan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int
 template <int IO, int D, int NB>
 hipError_t launch_tree_nb(const AttendTree &a, const TreePlan &p, hipStream_t stream)
 {
-    constexpr int R = 16 * NB;
+    constexpr int R = 32 * NB;
     attend_tree_kernel<IO, D, NB><<<dim3((unsigned)p.grid, a.kv.nk), 64 * kTreeWaves, 0, stream>>>(a, p.few);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.few.max_cut == 0) return e;
@@ -487,14 +647,11 @@ hipError_t launch_tree_nb(const AttendTree &a, const TreePlan &p, hipStream_t st
 template <int IO, int D>
 hipError_t launch_tree_d(const AttendTree &a, hipStream_t stream)
 {
-    const TreePlan p = make_plan(a.n_tokens, a.n_seqs, a.nq, a.kv.nk, D, a.kv.table_width, a.kv.block_size);
-    switch (p.nb) {
-    case 1: return launch_tree_nb<IO, D, 1>(a, p, stream);
-    case 2: return launch_tree_nb<IO, D, 2>(a, p, stream);
-    default:
-        if constexpr (D < 256) return launch_tree_nb<IO, D, 4>(a, p, stream);
-        return hipErrorInvalidValue;  // (the plan has none)
+    const TreePlan p = make_plan(a.n_tokens, a.n_seqs, a.nq, a.kv.nk, D, IO, a.kv.table_width, a.kv.block_size);
+    if constexpr (IO != kIoF32) {  // (fp32 queries of 64 rows have no room)
+        if (p.nb == 2) return launch_tree_nb<IO, D, 2>(a, p, stream);
     }
+    return launch_tree_nb<IO, D, 1>(a, p, stream);
 }
 
 template <int IO>
@@ -509,10 +666,10 @@ hipError_t launch_tree_io(const AttendTree &a, hipStream_t stream)
 
 }  // namespace
 
-size_t attend_tree_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int32_t table_width,
-                                   int32_t block_size)
+size_t attend_tree_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io,
+                                   int32_t table_width, int32_t block_size)
 {
-    return make_plan(n_tokens, n_seqs, nq, nk, head_dim, table_width, block_size).bytes;
+    return make_plan(n_tokens, n_seqs, nq, nk, head_dim, io, table_width, block_size).bytes;
 }
 
 hipError_t launch_attend_tree(const AttendTree &a, int io, hipStream_t stream)

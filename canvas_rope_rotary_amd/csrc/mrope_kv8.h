@@ -64,8 +64,8 @@ hipError_t launch_append(const Append &a, const Rotary &r, int io, hipStream_t s
 size_t attend_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io,
                               bool one_token, int32_t table_width, int32_t block_size);
 hipError_t launch_attend(const Attend &a, int io, hipStream_t stream);
-size_t attend_tree_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int32_t table_width,
-                                   int32_t block_size);
+size_t attend_tree_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io,
+                                   int32_t table_width, int32_t block_size);
 hipError_t launch_attend_tree(const AttendTree &a, int io, hipStream_t stream);
 
 #if defined(__HIPCC__)

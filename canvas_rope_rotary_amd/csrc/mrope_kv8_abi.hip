@@ -391,11 +391,10 @@ mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_hea
 size_t mrope_attend_tree_kv8_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
                                              int32_t head_dim, int32_t dtype, int32_t table_width, int32_t block_size)
 {
-    (void)dtype;
     if (n_tokens <= 0 || n_seqs <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads || table_width <= 0 ||
         block_size <= 0)
         return 0;
-    return attend_tree_workspace_bytes(n_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, table_width, block_size);
+    return attend_tree_workspace_bytes(n_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, dtype, table_width, block_size);
 }
 
 mrope_status mrope_attend_tree_kv8(const void *q, int64_t q_tok_stride, int64_t q_head_stride, int32_t n_q_heads,
@@ -416,6 +415,7 @@ mrope_status mrope_attend_tree_kv8(const void *q, int64_t q_tok_stride, int64_t 
                                          block_size, num_blocks, cache_block_stride, cache_tok_stride, cache_head_stride,
                                          softmax_scale, out, out_tok_stride, out_head_stride, lse, workspace, workspace_bytes, true, a);
     if (st != MROPE_OK) return st;
+    if (cache_tok_stride >= 1 << 28) return fail(MROPE_ERR_UNSUPPORTED, "cache_tok_stride must be below 2^28 (got %lld)", (long long)cache_tok_stride);
     if (mask_words < 1 || mask_words > 64) return fail(MROPE_ERR_ARG, "mask_words must be in [1, 64] (got %d)", mask_words);
     if (!aligned(mask, 8) || !aligned(context_lens, 4)) return fail(MROPE_ERR_ALIGN, "mask must be 8-byte, context_lens 4-byte aligned");
     if (a.n_tokens == 0) return MROPE_OK;
