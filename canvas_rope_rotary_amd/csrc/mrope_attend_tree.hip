@@ -29,7 +29,6 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kTreeWaves = kFewWaves;
 template <int IO>
 constexpr int kQTerms = IO == kIoF32 ? 3 : 1;
 template <int IO>
@@ -65,17 +64,20 @@ struct alignas(16) Block {
     uint8_t k[32 * D], v[32 * D];
 };
 
-template <int IO, int D, int NB>
+// A workgroup: WAVES waves, GROUPS groups of which take other rows of the same tokens; a wave has 32 * NB rows.
+template <int IO, int D, int NB, int GROUPS, int WAVES>
 struct alignas(16) TreeLds {
-    static constexpr bool kQueries = NB > 1;  // the queries are here
+    static constexpr int kShares = WAVES / GROUPS;                // waves with the same rows
+    static constexpr int kBuffers = GROUPS > 1 ? 2 : 1;
+    static constexpr int kSlice = kShares > 4 ? 16 : 32;       // rows whose parts meet at a time
     union {
         struct {
-            Block<D> ring[kTreeWaves][2];                        // of each wave: this block and the next
-            u32x4 q[kQueries ? NB : 0][kQTerms<IO>][D / 16][64];  // the operand's pieces by lane
+            Block<D> ring[kShares][kBuffers];                     // blocks of the waves with the same tokens
+            u32x4 q[NB * GROUPS][kQTerms<IO>][D / 16][64];    // the operand's pieces by lane
         };
-        struct {                                                 // when the last block is done
-            float o[kTreeWaves][32][D + 4];                      // thirty-two rows' parts
-            float ml[kTreeWaves][32 * NB][2];
+        struct {                                                  // when the last block is done
+            float o[kShares][kSlice][D + 4];
+            float ml[kShares][32 * NB * GROUPS][2];
         };
     };
 };
@@ -122,21 +124,8 @@ __device__ __forceinline__ VPiece<D> load_vpiece(const uint8_t *p)
     return r;
 }
 
-// Workgroups of a compute unit that LDS and the registers let run at once.
-constexpr int tree_resident(int io, int head_dim, int nb)
-{
-    if (head_dim == 256 || (io == kIoF32 && head_dim == 128)) return 1;
-    if (head_dim == 128 || nb > 1 || io == kIoF32) return 2;
-    return 3;
-}
-
-// The output's sums stay where they are: with one workgroup a compute unit in the accumulation registers.
-template <int IO, int D, int NB>
-__device__ __forceinline__ void pin(f32x16 &x)
-{
-    if constexpr (tree_resident(IO, D, NB) == 1) asm volatile("" : "+a"(x));
-    else asm volatile("" : "+v"(x));
-}
+// Workgroups of a compute unit that run at once: LDS holds one of 256 dims, and the registers two waves a SIMD.
+constexpr int tree_resident(int io, int head_dim, int nb) { return head_dim == 64 && io != kIoF32 && nb == 1 ? 2 : 1; }
 
 // The largest of three (of the others where one is NaN), without the canonicalisation that fmaxf costs.
 __device__ __forceinline__ float max3(float x, float y, float z)
@@ -156,15 +145,16 @@ __device__ __forceinline__ float max_halves(float x)
 // V's page scale (2^8 smaller) beside which the running maximum follows at once.
 constexpr float kLargeScale = 0x1p72f;
 
-template <int IO, int D, int NB>
-__global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void attend_tree_kernel(AttendTree a, FewPlan p)
+template <int IO, int D, int NB, int GROUPS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) void attend_tree_kernel(AttendTree a, FewPlan p)
 {
-    constexpr int R = 32 * NB, QT = kQTerms<IO>, N = kPTerms<IO>;
+    constexpr int R = 32 * NB * GROUPS, QT = kQTerms<IO>, N = kPTerms<IO>, kShares = WAVES / GROUPS;
     constexpr int NS = D / 16;   // steps of a score
     constexpr int NO = D / 32;   // dims of V that a lane holds of a token, and 32-dim tiles of O^T
     const Kv8 &kv = a.kv;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int col = lane & 31, half = lane >> 5;
+    const int share = wave % kShares, row0 = wave / kShares * 32 * NB;  // the wave's tokens, its first row of the tile
     const int g = a.nq / kv.nk, kvh = blockIdx.y;
 
     Cut cut = {0, 0, 0, 1};
@@ -193,10 +183,10 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
     const int32_t c0 = __builtin_amdgcn_readfirstlane((int32_t)min((int64_t)z * chunk, (int64_t)seen));
     const int32_t c1 = __builtin_amdgcn_readfirstlane(min(c0 + chunk, seen));
 
-    __shared__ TreeLds<IO, D, NB> lds;
+    __shared__ TreeLds<IO, D, NB, GROUPS, WAVES> lds;
 
-    // Blocks of 32 tokens: this wave's i-th begins at c0 + (4 i + wave) * 32.  Pages of 32 of them at a time, those of a
-    // sixteen of tokens a lane.
+    // Blocks of 32 tokens: this wave's i-th begins at c0 + (i kShares + share) * 32.  Pages of 32 of them at a time, those
+    // of a sixteen of tokens a lane.
     const int32_t *table = kv.tables + tl.s * kv.table_stride;
     int64_t base;
     float ks_lane, vs_lane;
@@ -205,7 +195,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
         base = 0;
         ks_lane = vs_lane = 1.0f;
         bool valid = false;
-        const int64_t tok = (int64_t)c0 + ((i + (lane >> 1)) * kTreeWaves + wave) * 32 + (lane & 1) * 16;
+        const int64_t tok = (int64_t)c0 + ((i + (lane >> 1)) * kShares + share) * 32 + (lane & 1) * 16;
         if (tok < c1) {
             const int32_t page = table[tok >> kv.bs_shift];
             valid = page >= 0 && page < kv.num_blocks;
@@ -222,42 +212,49 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
         float ks0, ks1, vs0, vs1;
         bool ok0, ok1;
     };
-    Info next;
-    Block<D> *ring = lds.ring[wave];
+    constexpr bool kTogether = GROUPS > 1;  // waves with other rows of the same tokens share a block
+    Block<D> *ring = lds.ring[share];
     // An instruction brings 1 KB: RI rows, and the lanes' places within them.
     constexpr int RI = 1024 / D, NI = 32 / RI, PR = D / 16;
     constexpr int KV = 16 / RI < NI ? 16 / RI : NI;  // places that differ: K's order of pieces goes by a row of sixteen
-    uint32_t koff[KV], voff[2];
+    uint32_t koff[KV], voff[1];
 #pragma unroll
     for (int i = 0; i < KV; ++i) koff[i] = (lane / PR) * (uint32_t)kv.c_tok + 16 * key_piece_of<D>(i * RI + lane / PR, lane % PR);
+    voff[0] = value_row_of<D>(lane / PR) * (uint32_t)kv.c_tok + 16 * (lane % PR);
+    auto fetch = [&](int i, const uint8_t *cache, const auto &off, uint8_t *to) {
+        constexpr int kPeriod = sizeof(off) / 4;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) voff[i] = (value_row_of<D>(i * RI + lane / PR) - i * RI) * (uint32_t)kv.c_tok + 16 * (lane % PR);
-    auto fetch = [&](int i) {  // block i, on its way to the ring
-        if (i && (i & 31) == 0) look_up(i);
-        const int at = 2 * (i & 31);
-        next.ks0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks_lane), at));
-        next.ks1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks_lane), at + 1));
-        next.vs0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs_lane), at));
-        next.vs1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs_lane), at + 1));
-        next.ok0 = (valid_mask >> at) & 1, next.ok1 = (valid_mask >> (at + 1)) & 1;
-        Block<D> &to = ring[i & 1];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)base, at + half);
-            const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)base >> 32), at + half);
+        for (int u = 0; u < 2; ++u) {
+            const int at = 2 * (i & 31) + u;
+            const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)base, at);
+            const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)base >> 32), at);
             const int64_t b = (int64_t)(((uint64_t)hi << 32) | lo);
 #pragma unroll
-            for (int j = half * NI / 2; j < (half + 1) * NI / 2; ++j)
-                to_lds16(kv.k + (b + (j * RI) % 16 * kv.c_tok), koff[j % KV], to.k + 1024 * j);
-#pragma unroll
-            for (int j = half * NI / 2; j < (half + 1) * NI / 2; ++j)
-                to_lds16(kv.v + (b + (j * RI) % 16 * kv.c_tok), voff[j & 1], to.v + 1024 * j);
+            for (int j = u * NI / 2; j < (u + 1) * NI / 2; ++j)
+                to_lds16(cache + (b + (j * RI) % 16 * kv.c_tok), off[j % kPeriod], to + 1024 * j);
         }
     };
-    const int n_all = (c1 - c0 + 31) / 32, n_mine = n_all > wave ? (n_all - wave + kTreeWaves - 1) / kTreeWaves : 0;
+    auto fetch_keys = [&](int i) {
+        if (i && (i & 31) == 0) look_up(i);
+        const int at = 2 * (i & 31);
+        Info x;
+        x.ks0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks_lane), at));
+        x.ks1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks_lane), at + 1));
+        x.vs0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs_lane), at));
+        x.vs1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs_lane), at + 1));
+        x.ok0 = (valid_mask >> at) & 1, x.ok1 = (valid_mask >> (at + 1)) & 1;
+        if (!kTogether || wave < kShares) fetch(i, kv.k, koff, ring[kTogether ? i & 1 : 0].k);
+        return x;
+    };
+    auto fetch_values = [&](int i) {
+        if (!kTogether || wave >= kShares) fetch(i, kv.v, voff, ring[kTogether ? i & 1 : 0].v);
+    };
+    const int n_all = (c1 - c0 + 31) / 32, n_mine = n_all > share ? (n_all - share + kShares - 1) / kShares : 0;
+    Info next{};
     if (n_mine > 0) {
         look_up(0);
-        fetch(0);
+        next = fetch_keys(0);
+        fetch_values(0);
     }
 
     // the scores' factor: its sign goes to Q, and zero makes Q zero, so the largest score is the largest sum
@@ -287,25 +284,18 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
                 }
             }
     };
-    constexpr bool kQueries = TreeLds<IO, D, NB>::kQueries;
-    u32x4 qreg[kQueries ? 1 : NS][QT];
-    if constexpr (kQueries) {
-        for (int e = threadIdx.x; e < NB * NS * 64; e += 64 * kTreeWaves) {
-            const int el = e & 63, s = (e >> 6) % NS, nb = (e >> 6) / NS;
-            u32x4 w[QT];
-            query_terms(nb * 32 + (el & 31), s, el >> 5, w);
+    for (int e = threadIdx.x; e < NB * GROUPS * NS * 64; e += 64 * WAVES) {
+        const int el = e & 63, s = (e >> 6) % NS, nb = (e >> 6) / NS;
+        u32x4 w[QT];
+        query_terms(nb * 32 + (el & 31), s, el >> 5, w);
 #pragma unroll
-            for (int t = 0; t < QT; ++t) lds.q[nb][t][s][el] = w[t];
-        }
-        __syncthreads();
-    } else {
-#pragma unroll
-        for (int s = 0; s < NS; ++s) query_terms(col, s, half, qreg[s]);
+        for (int t = 0; t < QT; ++t) lds.q[nb][t][s][el] = w[t];
     }
+    __syncthreads();
 
     int32_t itok[NB];  // the query token of this lane's row of each thirty-two
 #pragma unroll
-    for (int n = 0; n < NB; ++n) itok[n] = (tl.row0 + min(n * 32 + col, n_rows - 1)) / g;
+    for (int n = 0; n < NB; ++n) itok[n] = (tl.row0 + min(row0 + n * 32 + col, n_rows - 1)) / g;
     // Which of the tokens tok0 .. + 31 query token i sees: bit q for tok0 + q.
     auto sees = [&](int32_t i, int32_t tok0, bool ok0, bool ok1) {
         const int32_t j = tok0 - past;  // (the tree's token at tok0)
@@ -329,37 +319,41 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
         for (int i = 0; i < NO; ++i) {
 #pragma unroll
             for (int q = 0; q < 16; ++q) o[n][i][q] = 0.0f;
-            pin<IO, D, NB>(o[n][i]);
         }
     }
 
     uint32_t nan = 0;  // a block with a mask had one in V
-    for (int it = 0; it < n_mine; ++it) {
-        const int32_t tok0 = c0 + (it * kTreeWaves + wave) * 32;
-        // this block has come, and what was read of the one before it is there
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    const int n_loop = kTogether ? (n_all + kShares - 1) / kShares : n_mine;
+    for (int it = 0; it < n_loop; ++it) {
+        const int32_t tok0 = c0 + (it * kShares + share) * 32;
         const Info now = next;
-        const Block<D> &blk = ring[it & 1];
-        if (it + 1 < n_mine) fetch(it + 1);
+        const bool more = it + 1 < n_mine;
+        const Block<D> &blk = ring[kTogether ? it & 1 : 0];
+        if constexpr (kTogether) {  // this block has come, and the one before has been read: on to the next one
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (it >= n_mine) break;  // (the last round, in which some have no block)
+            if (more) {
+                next = fetch_keys(it + 1);
+                fetch_values(it + 1);
+            }
+        }
         const float kscale = col < 16 ? now.ks0 : now.ks1;
         int here = lane;  // (opaque: the queries stay in LDS and are read anew)
         asm volatile("" : "+v"(here));
 
-        // The scores, step by step, their operands read kAhead steps before their use.
-        constexpr int kSteps = kQueries ? NS * NB : 0, kAhead = kQueries ? 6 : 1;
-        u32x4 kp[NS / 2], q[kAhead];
-        auto query = [&](int i) { return lds.q[i % NB][0][i / NB][here]; };
+        // The scores, step by step, their operands read some steps before their use.
+        constexpr int kSteps = NS * NB * QT, kAhead = 4 < kSteps ? 4 : kSteps, kKeysAhead = 3 < NS / 2 ? 3 : NS / 2;
+        u32x4 kp[kKeysAhead], q[kAhead];
+        const u32x4 *queries = &lds.q[wave / kShares * NB][0][0][0];
+        auto query = [&](int i) { return queries[((i % NB * QT + i / NB % QT) * NS + i / (NB * QT)) * 64 + here]; };
+        auto key_piece = [&](int k) { return *reinterpret_cast<const u32x4 *>(blk.k + col * D + 16 * key_piece_of<D>(col, 2 * k + half)); };
 #pragma unroll
-        for (int k = 0; k < NS / 2; ++k) {
-            kp[k] = *reinterpret_cast<const u32x4 *>(blk.k + col * D + 16 * key_piece_of<D>(col, 2 * k + half));
-            if constexpr (kQueries) {
-                if (k == 0) {
+        for (int i = 0; i < kAhead; ++i) q[i] = query(i);
+        // this block's keys have come (its values, NI instructions, may be on their way)
+        if constexpr (!kTogether) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NI) : "memory");
 #pragma unroll
-                    for (int i = 0; i < kAhead; ++i)
-                        if (i < kSteps) q[i] = query(i);
-                }
-            }
-        }
+        for (int k = 0; k < kKeysAhead; ++k) kp[k] = key_piece(k);
         f32x16 s[NB];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -368,30 +362,25 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
+            const u32x4 x = kp[(k >> 1) % kKeysAhead];
             const int h = k & 1;
-            const u32x4 f = {key_pair<IO, false>(kp[k >> 1][2 * h], kscale), key_pair<IO, true>(kp[k >> 1][2 * h], kscale),
-                             key_pair<IO, false>(kp[k >> 1][2 * h + 1], kscale), key_pair<IO, true>(kp[k >> 1][2 * h + 1], kscale)};
-            if constexpr (kQueries) {
+            const u32x4 f = {key_pair<IO, false>(x[2 * h], kscale), key_pair<IO, true>(x[2 * h], kscale),
+                             key_pair<IO, false>(x[2 * h + 1], kscale), key_pair<IO, true>(x[2 * h + 1], kscale)};
+            if (h && (k >> 1) + kKeysAhead < NS / 2) kp[(k >> 1) % kKeysAhead] = key_piece((k >> 1) + kKeysAhead);
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const int i = k * NB + n;
+                    const int i = (k * QT + t) * NB + n;
                     s[n] = mfma_scores<IO>(f, q[i % kAhead], s[n]);
                     if (i + kAhead < kSteps) q[i % kAhead] = query(i + kAhead);
                 }
-                __builtin_amdgcn_sched_barrier(0);
-            } else {
-#pragma unroll
-                for (int t = 0; t < QT; ++t) s[0] = mfma_scores<IO>(f, qreg[k][t], s[0]);
-            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // V's bytes: step u of sixteen tokens, tokens 16 u + 8 a + 4 half + b
-        VPiece<D> vp[2][8];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                vp[u][j] = load_vpiece<D>(blk.v + value_row_of<D>(16 * u + 8 * (j >> 2) + 4 * half + (j & 3)) * D + col * NO);
-        __builtin_amdgcn_sched_barrier(0);
+        if (!kTogether && more) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the keys have been read
+            next = fetch_keys(it + 1);
+        }
 
         const bool edge = tok0 + 32 > open || !now.ok0 || !now.ok1;  // wave-uniform
         // (fp16: not 0, which would make a masked -infinity NaN, nor past fp32)
@@ -400,7 +389,7 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
         // the maximum moves only where it has grown by 2^8: until then p exceeds 1 and nothing is lost (but
         // beside large values, where the sums have no room for it, it moves at once)
         const float lag = fmaxf(now.vs0, now.vs1) >= kLargeScale ? 0.0f : 8.0f;
-        u32x4 pf[NB][2][N];  // P's terms by step
+        u32x4 pf[NB][2][N];  // P's terms by step of sixteen tokens
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             if (edge) {
@@ -419,20 +408,14 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
                 const float c = __builtin_amdgcn_exp2f(m[n] - m_new);
                 l[n] *= c;
 #pragma unroll
-                for (int i = 0; i < NO; ++i) {
-                    pin<IO, D, NB>(o[n][i]);
-                    o[n][i] *= c;
-                    pin<IO, D, NB>(o[n][i]);
-                }
+                for (int i = 0; i < NO; ++i) o[n][i] *= c;
                 m[n] = m_new;
             }
-            float add[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
                 float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e], e < 8 ? f0 : f1, -m[n]));
                 float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][e + 1], e < 8 ? f0 : f1, -m[n]));
-                add[0] += p0;
-                add[1] += p1;
+                l[n] += p0 + p1;
 #pragma unroll
                 for (int t = 0; t < N; ++t) {
                     const uint32_t w = pack16x2<kIoBF16>(p0, p1);
@@ -445,9 +428,20 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
                     }
                 }
             }
-            l[n] += add[0] + add[1];
         }
 
+        // this block's values have come (the next one's keys may be on their way)
+        if constexpr (!kTogether) {
+            if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NI) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        // V's bytes: step u of sixteen tokens, tokens 16 u + 8 a + 4 half + b
+        VPiece<D> vp[2][8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                vp[u][j] = load_vpiece<D>(blk.v + value_row_of<D>(16 * u + 8 * (j >> 2) + 4 * half + (j & 3)) * D + col * NO);
         // A NaN that some rows see and others do not, or that nobody sees, must not reach the product: the product
         // goes on without it, and the rows that see it are told at the end.
         if (edge) {
@@ -489,17 +483,17 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
                         for (int n = 0; n < NB; ++n) o[n][4 * w + e] = mfma_bf16(fv, pf[n][u][t], o[n][4 * w + e]);
                 }
             }
+            if (!kTogether && u == 1 && more) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the values have been read
+                fetch_values(it + 1);
+            }
         }
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < NO; ++i) pin<IO, D, NB>(o[n][i]);
     }
 
     if (__any(nan != 0)) {  // (rare) the blocks with a mask again: the rows that see a NaN have it in these dims
 #pragma unroll 1
         for (int it = 0; it < n_mine; ++it) {
-            const int32_t tok0 = c0 + (it * kTreeWaves + wave) * 32;
+            const int32_t tok0 = c0 + (it * kShares + share) * 32;
             if ((it & 31) == 0) look_up(it);
             const int at = 2 * (it & 31);
             const bool ok0 = (valid_mask >> at) & 1, ok1 = (valid_mask >> (at + 1)) & 1;
@@ -531,11 +525,9 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
 #pragma unroll
                         for (int e = 0; e < 16; ++e) cnt[e] = 0.0f;
                         cnt = mfma_bf16(ind, mine, cnt);
-                        pin<IO, D, NB>(o[n][i]);
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             if (cnt[e] > 0.0f) o[n][i][e] = __builtin_nanf("");
-                        pin<IO, D, NB>(o[n][i]);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
@@ -543,46 +535,50 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
         }
     }
 
-    // the waves' parts meet in LDS, thirty-two rows at a time
+    // the parts of the waves with the same rows meet in LDS, some rows at a time
     __syncthreads();  // (the ring and the queries have been read)
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         l[n] += __shfl_xor(l[n], 32);
         if (half == 0) {
-            lds.ml[wave][n * 32 + col][0] = m[n];
-            lds.ml[wave][n * 32 + col][1] = l[n];
+            lds.ml[share][row0 + n * 32 + col][0] = m[n];
+            lds.ml[share][row0 + n * 32 + col][1] = l[n];
         }
     }
     const bool whole = cut.n == 1;
     Partial<D, R> *part = reinterpret_cast<Partial<D, R> *>(static_cast<char *>(a.workspace) + cut_list_bytes(p.max_cut)) +
                           ((int64_t)(cut.slot + z) * kv.nk + kvh);
+    constexpr int kSlice = TreeLds<IO, D, NB, GROUPS, WAVES>::kSlice, kSlices = 32 / kSlice;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        if (n * 32 >= n_rows) break;
-        if (n) __syncthreads();  // the rows before have been read
+    for (int w = 0; w < NB * kSlices * GROUPS; ++w) {
+        const int n = w / kSlices % NB, slice = w % kSlices, first = w / (kSlices * NB) * 32 * NB + n * 32 + slice * kSlice;
+        if (first >= n_rows) continue;
+        if (w) __syncthreads();  // the rows before have been read
+        if (wave / kShares == w / (kSlices * NB) && col / kSlice == slice) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            float *dst = &lds.o[wave][col][(8 * (e >> 2) + 4 * half + (e & 3)) * NO];
-            if constexpr (NO >= 4) {
+            for (int e = 0; e < 16; ++e) {
+                float *dst = &lds.o[share][col % kSlice][(8 * (e >> 2) + 4 * half + (e & 3)) * NO];
+                if constexpr (NO >= 4) {
 #pragma unroll
-                for (int i = 0; i < NO; i += 4) *reinterpret_cast<f32x4 *>(dst + i) = f32x4{o[n][i][e], o[n][i + 1][e], o[n][i + 2][e], o[n][i + 3][e]};
-            } else {
+                    for (int i = 0; i < NO; i += 4) *reinterpret_cast<f32x4 *>(dst + i) = f32x4{o[n][i][e], o[n][i + 1][e], o[n][i + 2][e], o[n][i + 3][e]};
+                } else {
 #pragma unroll
-                for (int i = 0; i < NO; ++i) dst[i] = o[n][i][e];
+                    for (int i = 0; i < NO; ++i) dst[i] = o[n][i][e];
+                }
             }
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < min(32, n_rows - n * 32) * (D / 8); e += 64 * kTreeWaves) {
-            const int r32 = e / (D / 8), rr = n * 32 + r32, d = e % (D / 8) * 8;
+        for (int e = threadIdx.x; e < min(kSlice, n_rows - first) * (D / 8); e += 64 * WAVES) {
+            const int r = e / (D / 8), rr = first + r, d = e % (D / 8) * 8;
             float mm = kNoMax, ll = 0.0f, y[8] = {};
 #pragma unroll
-            for (int w = 0; w < kTreeWaves; ++w) mm = fmaxf(mm, lds.ml[w][rr][0]);
+            for (int i = 0; i < kShares; ++i) mm = fmaxf(mm, lds.ml[i][rr][0]);
 #pragma unroll
-            for (int w = 0; w < kTreeWaves; ++w) {
-                const float f = __builtin_amdgcn_exp2f(lds.ml[w][rr][0] - mm);
-                ll += lds.ml[w][rr][1] * f;
+            for (int i = 0; i < kShares; ++i) {
+                const float f = __builtin_amdgcn_exp2f(lds.ml[i][rr][0] - mm);
+                ll += lds.ml[i][rr][1] * f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] += lds.o[w][r32][d + i] * f;
+                for (int j = 0; j < 8; ++j) y[j] += lds.o[i][r][d + j] * f;
             }
             if (whole) {
                 const int rw = tl.row0 + rr;
@@ -608,11 +604,24 @@ __global__ __launch_bounds__(64 * kTreeWaves, tree_resident(IO, D, NB)) void att
 
 // ------------------------------------------------------------------ launchers ------------------
 struct TreePlan {
-    int nb;         // thirty-twos of rows of a tile
+    bool wide;      // tiles of 64 rows, else of 32
     int64_t tiles, grid;
     FewPlan few;
     size_t bytes;   // of the workspace
 };
+
+struct Shape {
+    int nb, groups, waves;  // (see the kernel)
+    constexpr int rows() const { return 32 * nb * groups; }
+};
+
+// fp32 queries take three times the room in LDS: tiles of 32 rows, and of 256 dims four waves.
+constexpr Shape shape_of(int io, int head_dim, bool wide)
+{
+    if (io == kIoF32) return {1, 1, head_dim == 256 ? 4 : 8};
+    if (!wide) return {1, 1, 8};
+    return head_dim == 256 ? Shape{1, 2, 8} : Shape{2, 1, 8};
+}
 
 TreePlan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int32_t head_dim, int io, int32_t table_width,
                    int32_t block_size)
@@ -620,10 +629,11 @@ TreePlan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int
     TreePlan p{};
     const int64_t g = nq / nk, cap = std::max<int64_t>(1, (int64_t)table_width * block_size);
     const int64_t seq_rows = (n_tokens * g + n_seqs - 1) / n_seqs;
-    p.nb = seq_rows <= 32 || io == kIoF32 ? 1 : 2;
-    const int64_t rows = 32 * p.nb, most = (cap + kFewUnit - 1) / kFewUnit;
+    p.wide = seq_rows > 32 && io != kIoF32;
+    const Shape shape = shape_of(io, head_dim, p.wide);
+    const int64_t rows = shape.rows(), most = (cap + kFewUnit - 1) / kFewUnit;
     p.tiles = n_tokens * g / rows + n_seqs;
-    p.few.budget = std::max(1, 256 * tree_resident(io, head_dim, p.nb) / nk);
+    p.few.budget = std::max(1, 256 * tree_resident(io, head_dim, shape.nb) / nk);
     p.grid = std::min(p.tiles + p.few.budget, p.tiles * most);
     if (most > 1) {
         p.few.max_cut = (int32_t)std::min<int64_t>(p.tiles, p.few.budget);
@@ -633,14 +643,14 @@ TreePlan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int
     return p;
 }
 
-template <int IO, int D, int NB>
-hipError_t launch_tree_nb(const AttendTree &a, const TreePlan &p, hipStream_t stream)
+template <int IO, int D, bool WIDE>
+hipError_t launch_tree_shape(const AttendTree &a, const TreePlan &p, hipStream_t stream)
 {
-    constexpr int R = 32 * NB;
-    attend_tree_kernel<IO, D, NB><<<dim3((unsigned)p.grid, a.kv.nk), 64 * kTreeWaves, 0, stream>>>(a, p.few);
+    constexpr Shape S = shape_of(IO, D, WIDE);
+    attend_tree_kernel<IO, D, S.nb, S.groups, S.waves><<<dim3((unsigned)p.grid, a.kv.nk), 64 * S.waves, 0, stream>>>(a, p.few);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.few.max_cut == 0) return e;
-    attend_join_kernel<IO, D, R, 1><<<dim3((unsigned)p.few.max_cut, a.kv.nk, R), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
+    attend_join_kernel<IO, D, S.rows(), 1><<<dim3((unsigned)p.few.max_cut, a.kv.nk, S.rows()), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
     return hipGetLastError();
 }
 
@@ -648,10 +658,10 @@ template <int IO, int D>
 hipError_t launch_tree_d(const AttendTree &a, hipStream_t stream)
 {
     const TreePlan p = make_plan(a.n_tokens, a.n_seqs, a.nq, a.kv.nk, D, IO, a.kv.table_width, a.kv.block_size);
-    if constexpr (IO != kIoF32) {  // (fp32 queries of 64 rows have no room)
-        if (p.nb == 2) return launch_tree_nb<IO, D, 2>(a, p, stream);
+    if constexpr (IO != kIoF32) {
+        if (p.wide) return launch_tree_shape<IO, D, true>(a, p, stream);
     }
-    return launch_tree_nb<IO, D, 1>(a, p, stream);
+    return launch_tree_shape<IO, D, false>(a, p, stream);
 }
 
 template <int IO>
