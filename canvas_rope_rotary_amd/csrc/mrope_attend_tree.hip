@@ -322,22 +322,16 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
         }
     }
 
-    uint32_t nan = 0;  // a block with a mask had one in V
-    const int n_loop = kTogether ? (n_all + kShares - 1) / kShares : n_mine;
-    for (int it = 0; it < n_loop; ++it) {
+    uint32_t nan = 0;    // a block with a mask had one in V
+    u32x4 pf[NB][2][N];  // P's terms by step of sixteen tokens
+    Info now{};          // of the block that the wave is at
+    bool edge = false;   // it has a mask (wave-uniform)
+
+    // Block `it`: its scores and their softmax.
+    auto scores = [&](int it, bool more) {
         const int32_t tok0 = c0 + (it * kShares + share) * 32;
-        const Info now = next;
-        const bool more = it + 1 < n_mine;
         const Block<D> &blk = ring[kTogether ? it & 1 : 0];
-        if constexpr (kTogether) {  // this block has come, and the one before has been read: on to the next one
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
-            if (it >= n_mine) break;  // (the last round, in which some have no block)
-            if (more) {
-                next = fetch_keys(it + 1);
-                fetch_values(it + 1);
-            }
-        }
+        now = next;
         const float kscale = col < 16 ? now.ks0 : now.ks1;
         int here = lane;  // (opaque: the queries stay in LDS and are read anew)
         asm volatile("" : "+v"(here));
@@ -350,8 +344,12 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
         auto key_piece = [&](int k) { return *reinterpret_cast<const u32x4 *>(blk.k + col * D + 16 * key_piece_of<D>(col, 2 * k + half)); };
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) q[i] = query(i);
-        // this block's keys have come (its values, NI instructions, may be on their way)
+        // its keys have come (its values, NI instructions, may be on their way)
         if constexpr (!kTogether) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NI) : "memory");
+        else if (more) {
+            next = fetch_keys(it + 1);
+            fetch_values(it + 1);
+        }
 #pragma unroll
         for (int k = 0; k < kKeysAhead; ++k) kp[k] = key_piece(k);
         f32x16 s[NB];
@@ -382,14 +380,13 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
             next = fetch_keys(it + 1);
         }
 
-        const bool edge = tok0 + 32 > open || !now.ok0 || !now.ok1;  // wave-uniform
+        edge = tok0 + 32 > open || !now.ok0 || !now.ok1;
         // (fp16: not 0, which would make a masked -infinity NaN, nor past fp32)
         const float f0 = IO == kIoF16 ? fminf(fmaxf(now.ks0 * factor, 0x1p-126f), 0x1p127f) : factor;
         const float f1 = IO == kIoF16 ? fminf(fmaxf(now.ks1 * factor, 0x1p-126f), 0x1p127f) : factor;
         // the maximum moves only where it has grown by 2^8: until then p exceeds 1 and nothing is lost (but
         // beside large values, where the sums have no room for it, it moves at once)
         const float lag = fmaxf(now.vs0, now.vs1) >= kLargeScale ? 0.0f : 8.0f;
-        u32x4 pf[NB][2][N];  // P's terms by step of sixteen tokens
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             if (edge) {
@@ -430,8 +427,12 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
             }
         }
 
-        // this block's values have come (the next one's keys may be on their way)
-        if constexpr (!kTogether) {
+    };
+
+    // Then its product with V.
+    auto product = [&](int it, bool more) {
+        const Block<D> &blk = ring[kTogether ? it & 1 : 0];
+        if constexpr (!kTogether) {  // its values have come (the next block's keys may be on their way)
             if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NI) : "memory");
             else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
@@ -488,6 +489,34 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
                 fetch_values(it + 1);
             }
         }
+    };
+
+    if constexpr (!kTogether) {
+        for (int it = 0; it < n_mine; ++it) {
+            scores(it, it + 1 < n_mine);
+            product(it, it + 1 < n_mine);
+        }
+    } else {
+        // The two groups take turns: while one is at a block's scores and softmax, the other is at a product, so a SIMD's
+        // two waves want the matrix unit and the vector unit at different times.  Between two barriers the first group takes
+        // block i's scores while the second takes block i - 1's product, then block i's product while the second takes its
+        // scores.  The first group brings keys, the second values, both at the start of their scores: a block two
+        // barriers before anyone wants it, to where the block before last was, which nobody reads any more.
+        static_assert(GROUPS == 2, "two groups take turns");
+        const int n_loop = (n_all + kShares - 1) / kShares;
+        if (wave >= kShares) __syncthreads();
+        for (int it = 0; it < n_mine; ++it) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what this wave asked for has come
+            __syncthreads();
+            scores(it, it + 1 < n_mine);
+            __syncthreads();
+            product(it, it + 1 < n_mine);
+        }
+        if (n_mine < n_loop) {  // (a last round in which this wave has no block)
+            __syncthreads();
+            __syncthreads();
+        }
+        if (wave < kShares) __syncthreads();
     }
 
     if (__any(nan != 0)) {  // (rare) the blocks with a mask again: the rows that see a NaN have it in these dims
