@@ -165,7 +165,7 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
     } else {
         CutList *list = static_cast<CutList *>(a.workspace);
         int32_t rank, n_cut;
-        const bool found = find_chunk<R>(a, g, blockIdx.x, p.budget, lane, cut, z, rank, n_cut);
+        const bool found = find_chunk<R, true>(a, g, blockIdx.x, p.budget, lane, cut, z, rank, n_cut);
         if (blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) list->n = min(n_cut, p.max_cut);
         if (!found) return;
         if (cut.n > 1) {
@@ -663,10 +663,10 @@ TreePlan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int
     const int64_t rows = shape.rows(), most = (cap + kFewUnit - 1) / kFewUnit;
     p.tiles = n_tokens * g / rows + n_seqs;
     p.few.budget = std::max(1, 256 * tree_resident(io, head_dim, shape.nb) / nk);
-    p.grid = std::min(p.tiles + p.few.budget, p.tiles * most);
+    p.grid = std::min(std::max<int64_t>(p.tiles, p.few.budget), p.tiles * most);
     if (most > 1) {
         p.few.max_cut = (int32_t)std::min<int64_t>(p.tiles, p.few.budget);
-        p.few.max_slots = (int32_t)std::min<int64_t>(2 * p.few.budget, p.tiles * most);
+        p.few.max_slots = (int32_t)std::min<int64_t>(p.few.budget, p.tiles * most);
         p.bytes = cut_list_bytes(p.few.max_cut) + (size_t)(rows * (head_dim + 2) * 4) * nk * (size_t)p.few.max_slots;
     }
     return p;
@@ -679,7 +679,12 @@ hipError_t launch_tree_shape(const AttendTree &a, const TreePlan &p, hipStream_t
     attend_tree_kernel<IO, D, S.nb, S.groups, S.waves><<<dim3((unsigned)p.grid, a.kv.nk), 64 * S.waves, 0, stream>>>(a, p.few);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.few.max_cut == 0) return e;
-    attend_join_kernel<IO, D, S.rows(), 1><<<dim3((unsigned)p.few.max_cut, a.kv.nk, S.rows()), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
+    // (as many chunks a tile as the budget has for the tiles there may be, or some more)
+    const unsigned tiles = (unsigned)p.few.max_cut;
+    if (p.few.max_slots > kJoinMany * p.few.max_cut)
+        attend_join_kernel<IO, D, S.rows(), 1><<<dim3(tiles, a.kv.nk, S.rows()), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
+    else
+        attend_join_kernel<IO, D, S.rows(), 4><<<dim3(tiles, a.kv.nk, S.rows() / 4), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
     return hipGetLastError();
 }
 
