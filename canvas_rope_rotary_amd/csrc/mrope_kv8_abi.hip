@@ -469,7 +469,7 @@ mrope_status mrope_verify_tree(const void *target, int64_t target_stride, const 
         return fail(MROPE_ERR_ALIGN, "int32 and fp32 arrays must be 4-byte aligned");
     if (n_seqs == 0) return MROPE_OK;
     const VerifyPlan plan = verify_plan(n_seqs, vocab, draft && parents);
-    if ((int64_t)n_seqs * plan.n_chunks * 256 > kMaxGridThreads)
+    if ((int64_t)n_seqs * plan.n_sums * 256 > kMaxGridThreads)
         return fail(MROPE_ERR_ARG, "too many sequences for the vocabulary (%d, %d)", n_seqs, vocab);
     if (!n_kept || !next_ids || !u_next || !cu_seqlens) return fail(MROPE_ERR_ARG, "cu_seqlens / u_next / n_kept / next_ids is NULL");
     if (n_tokens > 0 && (!target || !ids || !u_accept || !path)) return fail(MROPE_ERR_ARG, "target / ids / u_accept / path is NULL");

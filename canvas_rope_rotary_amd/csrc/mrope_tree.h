@@ -50,8 +50,8 @@ struct alignas(16) Walk {
 
 struct VerifyPlan {
     int32_t rounds;     // launches that sum a row a sequence
-    int32_t chunk;      // elements of a workgroup
-    int32_t n_chunks;
+    int32_t share;      // sums of a workgroup
+    int32_t n_sums;     // of a row
 };
 
 struct KeepLayers {
