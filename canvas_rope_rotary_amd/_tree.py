@@ -7,24 +7,65 @@ from array import array
 import torch
 
 from . import _lib
-from ._kv8 import _code, _heads, _i32, _i32_out, _kv8, _same_device, _scratch, _stream_of, _tables
+from ._kv8 import _F8, _code, _heads, _kv8, _scratch, _stream_of, _tables
 from ._lib import _invoke, _on_device, load
 
 TREE_MAX_TOKENS = 1024
 MAX_LAYERS = 64
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_empty, _empty_like = torch.empty, torch.empty_like
+
+# As in the calls of the cache: a step of few sequences spends most of its time here, so each property of a
+# tensor is read once, and outputs are made like an input where one has their shape.
+
+
+def _device_of(first, others) -> int:
+    """Index of the one device that all tensors (None: not given) are on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("all tensors must be on a CUDA (HIP) device")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError("all tensors must be on the same CUDA (HIP) device")
+    return index
+
+
+def _vec(t, name: str, n: int, dtype=_I32) -> int:
+    """Address of a contiguous vector of n entries."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D {str(dtype)[6:]} tensor of {n} entries")
+    return t.data_ptr()
+
+
+def _offsets(t):
+    """(address, sequences) of cu_seqlens."""
+    if t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor")
+    return t.data_ptr(), t.shape[0] - 1
+
+
+def _tokens(t, name: str):
+    """(address, tokens) of an int32 vector with an entry a token."""
+    if t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
+    return t.data_ptr(), t.shape[0]
 
 
 def _mask(t, T: int):
     """(address, words) of a mask [tokens, words]."""
-    if t.dtype is not torch.int64 or t.dim() != 2 or t.shape[0] != T or not t.is_contiguous():
+    shape = t.shape
+    if t.dtype is not _I64 or len(shape) != 2 or shape[0] != T or not t.is_contiguous():
         raise ValueError("mask must be a contiguous int64 [tokens, words] tensor")
-    return t.data_ptr(), t.shape[1]
+    return t.data_ptr(), shape[1]
 
 
-def _f32(t, name: str, n: int) -> int:
-    if t.dtype is not torch.float32 or t.dim() != 1 or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name} must be a contiguous 1-D float32 tensor of {n} entries")
-    return t.data_ptr()
+def _call(index: int, cfunc, *args) -> None:
+    """The C call, on the tensors' device and its current stream."""
+    if torch._C._cuda_getDevice() == index:
+        _invoke(cfunc, *args, _stream_of(index))
+    else:
+        with _on_device(torch.device("cuda", index)):
+            _invoke(cfunc, *args, _stream_of(index))
 
 
 def _rows(t, name: str, dtype, T: int, vocab: int):
@@ -43,22 +84,22 @@ def planes_tree(parents: torch.Tensor, cu_seqlens: torch.Tensor, pos_offset: tor
     token 0, amount [n] int32 (None: 0).  Returns (planes int32 [3, T]: pos_offset + depth - amount, mask int64
     [T, mask_words]: bit b of word w is set if token 64 w + b of the sequence is the row's token or an ancestor
     of it), for apply_kv8 and attend_tree_kv8 of every layer."""
-    dev = _same_device(parents, cu_seqlens, pos_offset, amount, planes, mask)
-    T = parents.numel()
-    pp, cu = _i32(parents, "parents"), _i32(cu_seqlens, "cu_seqlens")
-    n = cu_seqlens.numel() - 1
-    off = _i32(pos_offset, "pos_offset", n)
-    am = None if amount is None else _i32(amount, "amount", n)
+    index = _device_of(parents, (cu_seqlens, pos_offset, amount, planes, mask))
+    pp, T = _tokens(parents, "parents")
+    cu, n = _offsets(cu_seqlens)
+    off = _vec(pos_offset, "pos_offset", n)
+    am = None if amount is None else _vec(amount, "amount", n)
     if planes is None:
-        planes = torch.empty((3, T), dtype=torch.int32, device=dev)
-    elif planes.dtype is not torch.int32 or planes.dim() != 2 or planes.shape[0] != 3 or planes.shape[1] < T or planes.stride(1) != 1:
-        raise ValueError("planes must be an int32 [3, >= tokens] tensor with unit column stride")
+        planes = _empty((3, T), dtype=_I32, device=parents.device)
+        stride = T
+    else:
+        stride = planes.stride(0)
+        if planes.dtype is not _I32 or planes.dim() != 2 or planes.shape[0] != 3 or planes.shape[1] < T or planes.stride(1) != 1:
+            raise ValueError("planes must be an int32 [3, >= tokens] tensor with unit column stride")
     if mask is None:
-        mask = torch.empty((T, int(mask_words)), dtype=torch.int64, device=dev)
+        mask = _empty((T, int(mask_words)), dtype=_I64, device=parents.device)
     mp, words = _mask(mask, T)
-    with _on_device(dev):
-        _invoke(load().mrope_planes_tree, pp, T, cu, n, off, am, planes.data_ptr(), planes.stride(0), mp, words,
-                _stream_of(dev.index))
+    _call(index, load().mrope_planes_tree, pp, T, cu, n, off, am, planes.data_ptr(), stride, mp, words)
     return planes, mask
 
 
@@ -69,32 +110,35 @@ def attend_tree_kv8(q: torch.Tensor, cu_seqlens: torch.Tensor, context_lens: tor
     """attend_kv8 under a mask over the query tokens: token i of a sequence of len sees the positions before
     context - len, and those of the sequence's tokens whose bits are set in its row of mask int64 [T, words]
     (see planes_tree).  Everything else as in attend_kv8.  Returns (out, lse or None)."""
-    dev = _same_device(q, cu_seqlens, context_lens, mask, block_tables, k_cache, v_cache, k_scale, v_scale, out, lse, workspace)
+    index = _device_of(q, (cu_seqlens, context_lens, mask, block_tables, k_cache, v_cache, k_scale, v_scale, out, lse, workspace))
     dt = _code(q)
     qp, qt, qh, nq, T, D = _heads(q, "q")
-    cu = _i32(cu_seqlens, "cu_seqlens")
-    n = cu_seqlens.numel() - 1
-    ctx = _i32(context_lens, "context_lens", n)
+    cu, n = _offsets(cu_seqlens)
+    ctx = _vec(context_lens, "context_lens", n)
     mp, words = _mask(mask, T)
     cache = _kv8(k_cache, v_cache, k_scale, v_scale, None, D)
     nk, bs, blocks = k_cache.shape[2], cache[4], cache[5]
     if out is None:
-        out = torch.empty((T, nq, D), dtype=q.dtype, device=dev)
-    op, ot, oh, no, _, _ = _heads(out, "out", q.dtype, T, D)
-    if no != nq:
-        raise ValueError("out must have q's shape")
-    if lse is None and return_lse:
-        lse = torch.empty((T, nq), dtype=torch.float32, device=dev)
-    if lse is not None and (lse.shape != (T, nq) or lse.dtype is not torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
+        out = _empty_like(q, memory_format=torch.contiguous_format)
+        op, ot, oh = out.data_ptr(), nq * D, D
+    else:
+        op, ot, oh, no, _, _ = _heads(out, "out", q.dtype, T, D)
+        if no != nq:
+            raise ValueError("out must have q's shape")
+    lp = None
+    if lse is not None:
+        if lse.shape != (T, nq) or lse.dtype is not _F32 or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
+    elif return_lse:
+        lse = _empty((T, nq), dtype=_F32, device=q.device)
+    if lse is not None:
+        lp = lse.data_ptr()
     tp, ts, tw = _tables(block_tables, n)
     lib = load()
     need = lib.mrope_attend_tree_kv8_workspace_bytes(T, n, nq, nk, D, dt, tw if blocks else 0, bs)
-    with _on_device(dev):
-        ws, ws_bytes, keep = _scratch(need, dev, workspace)
-        _invoke(lib.mrope_attend_tree_kv8, qp, qt, qh, nq, T, nk, D, dt, cu, n, ctx, mp, words, tp, ts, tw, *cache,
-                D ** -0.5 if softmax_scale is None else float(softmax_scale), op, ot, oh,
-                None if lse is None else lse.data_ptr(), ws, ws_bytes, _stream_of(dev.index))
+    ws, ws_bytes, keep = _scratch(need, q.device, workspace)
+    _call(index, lib.mrope_attend_tree_kv8, qp, qt, qh, nq, T, nk, D, dt, cu, n, ctx, mp, words, tp, ts, tw, *cache,
+          D ** -0.5 if softmax_scale is None else float(softmax_scale), op, ot, oh, lp, ws, ws_bytes)
     return out, lse
 
 
@@ -115,24 +159,26 @@ def verify_tree(target_probs: torch.Tensor, ids: torch.Tensor, parents: torch.Te
     distributions that each token's children were drawn from (None: they were not drawn).  Returns
     (n_kept [n]: accepted tokens, token 0 included; path [T]: their indices in order, then -1; next_ids [n]),
     all int32: n_kept and path are what keep_kv8 takes."""
-    dev = _same_device(target_probs, ids, parents, cu_seqlens, u_accept, u_next, draft_probs, n_kept, path, next_ids, workspace)
+    index = _device_of(target_probs, (ids, parents, cu_seqlens, u_accept, u_next, draft_probs, n_kept, path, next_ids, workspace))
     dt = _code(target_probs)
-    T, vocab = ids.numel(), target_probs.shape[-1]
-    ip = _i32(ids, "ids")
+    ip, T = _tokens(ids, "ids")
+    vocab = target_probs.shape[-1]
     tp, ts = _rows(target_probs, "target_probs", target_probs.dtype, T, vocab)
     dp, ds = (None, 0) if draft_probs is None else _rows(draft_probs, "draft_probs", target_probs.dtype, T, vocab)
-    pp = None if parents is None else _i32(parents, "parents", T)
-    cu = _i32(cu_seqlens, "cu_seqlens")
-    n = cu_seqlens.numel() - 1
-    ua, un = _f32(u_accept, "u_accept", T), _f32(u_next, "u_next", n)
-    n_kept, path = _i32_out(n_kept, "n_kept", n, dev), _i32_out(path, "path", T, dev)
-    next_ids = _i32_out(next_ids, "next_ids", n, dev)
+    pp = None if parents is None else _vec(parents, "parents", T)
+    cu, n = _offsets(cu_seqlens)
+    ua, un = _vec(u_accept, "u_accept", T, _F32), _vec(u_next, "u_next", n, _F32)
+    if path is None:
+        path = _empty_like(ids)
+    if n_kept is None:
+        n_kept = _empty_like(u_next, dtype=_I32)
+    if next_ids is None:
+        next_ids = _empty_like(n_kept)
     lib = load()
     need = lib.mrope_verify_tree_workspace_bytes(n, vocab, dp is not None, pp is not None)
-    with _on_device(dev):
-        ws, ws_bytes, keep = _scratch(need, dev, workspace)
-        _invoke(lib.mrope_verify_tree, tp, ts, dp, ds, vocab, dt, T, ip, pp, cu, n, ua, un, n_kept.data_ptr(), path.data_ptr(),
-                next_ids.data_ptr(), ws, ws_bytes, _stream_of(dev.index))
+    ws, ws_bytes, keep = _scratch(need, ids.device, workspace)
+    _call(index, lib.mrope_verify_tree, tp, ts, dp, ds, vocab, dt, T, ip, pp, cu, n, ua, un, _vec(n_kept, "n_kept", n),
+          _vec(path, "path", T), _vec(next_ids, "next_ids", n), ws, ws_bytes)
     return n_kept, path, next_ids
 
 
@@ -146,24 +192,30 @@ def keep_kv8(n_kept: torch.Tensor, path: torch.Tensor, cu_seqlens: torch.Tensor,
     caches = tuple(caches)
     if not caches:
         raise ValueError("caches is empty")
-    dev = _same_device(n_kept, path, cu_seqlens, pos_offset, block_tables, *(t for layer in caches for t in layer))
-    pp, T = _i32(path, "path"), path.numel()
-    cu = _i32(cu_seqlens, "cu_seqlens")
-    n = cu_seqlens.numel() - 1
-    kp, off = _i32(n_kept, "n_kept", n), _i32(pos_offset, "pos_offset", n)
-    shape, stride = caches[0][0].shape, caches[0][0].stride()
-    if len(shape) != 4:
-        raise ValueError("k_cache must be [num_blocks, block_size, n_kv_heads, head_dim]")
-    flat, rest = [], None
-    for k_cache, v_cache, k_scale, v_scale in caches:
-        if k_cache.shape != shape or k_cache.stride() != stride:
-            raise ValueError("the layers' caches must have one shape and the same strides")
-        one = _kv8(k_cache, v_cache, k_scale, v_scale, shape[2], shape[3])
-        flat += one[:4]
-        rest = one[4:]
-    arr = array("Q", flat)  # read by the call itself
+    layers = tuple(zip(*caches))
+    if len(layers) != 4 or any(len(layer) != 4 for layer in caches):
+        raise ValueError("caches must be (k_cache, v_cache, k_scale, v_scale) of each layer")
+    codes, scales = layers[0] + layers[1], layers[2] + layers[3]
+    index = _device_of(n_kept, (path, cu_seqlens, pos_offset, block_tables, *codes, *scales))
+    pp, T = _tokens(path, "path")
+    cu, n = _offsets(cu_seqlens)
+    kp, off = _vec(n_kept, "n_kept", n), _vec(pos_offset, "pos_offset", n)
+    k_cache = caches[0][0]
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or stride[3] != 1:
+        raise ValueError("k_cache must be [num_blocks, block_size, n_kv_heads, head_dim] with contiguous head_dim")
+    blocks, bs, nk, D = shape
+    per_head = (blocks, nk)
+    for t in codes:
+        if t.shape != shape or t.stride() != stride:
+            raise ValueError("the caches of all layers must have one shape and the same strides")
+        if t.dtype is not _F8 and t.dtype is not torch.uint8:
+            raise ValueError("caches must be float8_e4m3fn (or their codes in uint8)")
+    for t in scales:
+        if t.dtype is not _F32 or t.shape != per_head or not t.is_contiguous():
+            raise ValueError("scales must be contiguous float32 [num_blocks, n_kv_heads] tensors")
+    arr = array("Q", [t.data_ptr() for layer in caches for t in layer])  # read by the call itself
     if _lib._recording is not None:
         _lib._held.append(arr)
-    with _on_device(dev):
-        _invoke(load().mrope_keep_kv8, arr.buffer_info()[0], len(caches), shape[2], shape[3], *rest, kp, pp, T, cu, n, off,
-                *_tables(block_tables, n), _stream_of(dev.index))
+    _call(index, load().mrope_keep_kv8, arr.buffer_info()[0], len(caches), nk, D, bs, blocks, stride[0], stride[1], stride[2], kp, pp, T, cu,
+          n, off, *_tables(block_tables, n))
