@@ -196,10 +196,8 @@ struct Sums {  // of a range of sequences: chunks, tiles that are cut, chunks of
     }
 };
 
-// Chunk w of the call: `z` of tile `c`, whose place in the list of cut tiles is `rank`.  FIT: at most `budget` chunks in
-// all, or the tiles, none of them cut (each then adds less than one chunk to its share, so what the tiles leave of the
-// budget is shared).
-template <int R, bool FIT = false>
+// Chunk w of the call: `z` of tile `c`, whose place in the list of cut tiles is `rank`.
+template <int R>
 __device__ __forceinline__ bool find_chunk(const Attend &a, int g, int64_t w, int32_t budget, int lane, Cut &c, int32_t &z,
                                            int32_t &rank, int32_t &n_cut)
 {
@@ -207,22 +205,14 @@ __device__ __forceinline__ bool find_chunk(const Attend &a, int g, int64_t w, in
     const int64_t s0 = (int64_t)lane * per;
     int64_t total = 0;
     int32_t tiles = 0, seen = 0;
-    [[maybe_unused]] int32_t all_tiles = 0;
     for (int32_t i = 0; i < per; ++i) {
         const bool in = s0 + i < a.n_seqs;
         tiles = tiles_of<R>(a, g, (int32_t)(s0 + i), in);
         seen = seen_of(a, (int32_t)(s0 + i), in);
         total += (int64_t)tiles * seen;
-        if constexpr (FIT) all_tiles += tiles;
     }
 #pragma unroll
     for (int x = 1; x < 64; x *= 2) total += __shfl_xor(total, x);
-    if constexpr (FIT) {
-#pragma unroll
-        for (int x = 1; x < 64; x *= 2) all_tiles += __shfl_xor(all_tiles, x);
-        if (all_tiles >= budget) total = (int64_t)1 << 60;
-        else budget -= all_tiles;
-    }
     const int64_t want = (total + budget - 1) / budget;
     const int32_t unit = (int32_t)max(min((want + kFewUnit - 1) / kFewUnit * kFewUnit, (int64_t)1 << 28), (int64_t)kFewUnit);
 

@@ -57,6 +57,96 @@ __device__ __forceinline__ uint32_t key_pair(uint32_t u, float scale)
     else return bf16_pair<HI>(u, scale);
 }
 
+// Running sum over the lanes: within sixteens, then a sixteen's last to those behind it.
+__device__ __forceinline__ int32_t running(int32_t x)
+{
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+    return x;
+}
+
+// The work of workgroup `id`: a chunk of a tile, of chunks that are as long as one another and fit those that run at once:
+// at most `budget` a KV head, or the tiles, none of them cut.  A chunk is `unit` times U tokens, and a tile adds less than one
+// chunk to its share of the sum, so what the tiles leave of the budget is shared.  `z` is the chunk's place in its tile, `rank`
+// that of the tile in the list of cut ones.  The chunks of all heads in order, an eighth to each XCD (id % 8): tiles of the same
+// context and heads of the same pages meet in its L2.
+template <int R, int U>
+__device__ __forceinline__ bool find_fit(const AttendTree &a, int g, int32_t id, int32_t budget, int lane, Cut &c, int32_t &z,
+                                         int32_t &rank, int32_t &n_cut, int32_t &kvh, Tile &t)
+{
+    int32_t t0, len, ctx, seen, tiles, units;
+    auto read = [&](int32_t s) {
+        const int32_t at = min(s, a.n_seqs - 1), next = a.cu[at + 1], c_at = a.ctx[at];
+        t0 = a.cu[at];
+        len = s < a.n_seqs ? (int32_t)min((int64_t)next, a.n_tokens) - t0 : 0;
+        ctx = max(c_at, 0);
+        seen = (int32_t)min((int64_t)ctx, (int64_t)a.kv.table_width << a.kv.bs_shift);  // (at most 2^27)
+        tiles = (int32_t)(((int64_t)max(len, 0) * g + R - 1) / R);
+        units = (seen + U - 1) / U;
+    };
+    int32_t all = 0, total = 0;
+    for (int32_t s = lane; s - lane < a.n_seqs; s += 64) {
+        read(s);
+        all += tiles;
+        total += tiles * units;  // (matters where the tiles are fewer than the budget, and is below 2^31 then)
+    }
+    all = __builtin_amdgcn_readlane(running(all), 63);
+    total = __builtin_amdgcn_readlane(running(total), 63);
+    const int32_t left = budget - all;
+    const int32_t unit = left > 0 ? max((int32_t)(((uint32_t)total + left - 1) / (uint32_t)left), 1) : 1 << 30;
+    auto chunks_here = [&] { return max((int32_t)((uint32_t)(units + unit - 1) / (uint32_t)unit), 1); };
+    int32_t count = all;  // of chunks
+    if (left > 0) {
+        count = 0;
+        for (int32_t s = lane; s - lane < a.n_seqs; s += 64) {
+            if (a.n_seqs > 64) read(s);
+            count += tiles * chunks_here();
+        }
+        count = __builtin_amdgcn_readlane(running(count), 63);
+    }
+    const int32_t nk = a.kv.nk, share = (int32_t)(((int64_t)count * nk + 7) / 8), v = id % 8 * share + id / 8;
+    const bool mine = id / 8 < share && v < count * nk;
+    if (!mine && id) return false;
+    const int32_t w = mine ? v / nk : 1 << 30;
+    kvh = v % nk;
+
+    Sums base = {0, 0, 0};
+    bool found = false;
+    for (int32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
+        if (a.n_seqs > 64) read(s0 + lane);
+        const int32_t n = chunks_here();
+        const int32_t own = tiles * n, own_cut = n > 1 ? tiles : 0;
+        const int32_t up = running(own), up_cut = running(own_cut), up_slots = running(n > 1 ? own : 0);
+        if (!found && base.all + __builtin_amdgcn_readlane(up, 63) > w) {
+            found = true;
+            const int at = min(__builtin_popcountll(__ballot(base.all + up <= w)), 63);
+            c.s = s0 + at;
+            c.n = __builtin_amdgcn_readlane(n, at);
+            const int32_t k = w - base.all - __builtin_amdgcn_readlane(up - own, at);
+            c.tile = k / c.n;
+            z = k - c.tile * c.n;
+            c.slot = base.slots + __builtin_amdgcn_readlane(up_slots - (n > 1 ? own : 0), at) + c.tile * c.n;
+            rank = base.cut + __builtin_amdgcn_readlane(up_cut - own_cut, at) + c.tile;
+            t.s = c.s;
+            t.t0 = __builtin_amdgcn_readlane(t0, at);
+            t.rows = __builtin_amdgcn_readlane(len, at) * g;
+            t.row0 = c.tile * R;
+            t.seen = __builtin_amdgcn_readlane(seen, at);
+            t.past = (int64_t)__builtin_amdgcn_readlane(ctx, at) - __builtin_amdgcn_readlane(len, at);
+            if (id) break;  // (the first workgroup goes on, for the sum)
+        }
+        base.all += __builtin_amdgcn_readlane(up, 63);
+        base.cut += __builtin_amdgcn_readlane(up_cut, 63);
+        base.slots += __builtin_amdgcn_readlane(up_slots, 63);
+    }
+    n_cut = base.cut;
+    return found;
+}
+
 // Codes of 32 tokens on their way, as they lie in the cache but for the order of a row's 16-byte pieces (K) and of the
 // rows (V): so chosen that the lanes of a read lie in different banks.
 template <int D>
@@ -69,7 +159,7 @@ template <int IO, int D, int NB, int GROUPS, int WAVES>
 struct alignas(16) TreeLds {
     static constexpr int kShares = WAVES / GROUPS;                // waves with the same rows
     static constexpr int kBuffers = GROUPS > 1 ? 2 : 1;
-    static constexpr int kSlice = kShares > 4 ? 16 : 32;       // rows whose parts meet at a time
+    static constexpr int kSlice = kShares > 4 && D == 256 ? 16 : 32;  // rows whose parts meet at a time: as LDS has room
     union {
         struct {
             Block<D> ring[kShares][kBuffers];                     // blocks of the waves with the same tokens
@@ -83,11 +173,11 @@ struct alignas(16) TreeLds {
 };
 
 // 16 bytes a lane from global memory (g, the same in all lanes, and an offset) to LDS, where the lanes' lie one after
-// the other from `l` on.
+// the other from `l` on.  (A buffer load: for the global form the compiler waits at the next use of LDS for all of it.)
 __device__ __forceinline__ void to_lds16(const uint8_t *g, uint32_t off, uint8_t *l)
 {
-    typedef const __attribute__((address_space(1))) uint8_t *Global;
-    __builtin_amdgcn_global_load_lds((Global)g + off, (__attribute__((address_space(3))) void *)l, 16, 0, 0);
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(g), 0, -1, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)l, 16, off, 0, 0, 0);
 }
 
 // Where row r of 32 has its 16-byte piece p of K, and its row of V.
@@ -109,13 +199,14 @@ template <int D>
 struct VPiece {
     uint32_t w[D == 256 ? 2 : 1];
 };
+#define MROPE_LDS __attribute__((address_space(3)))
 template <int D>
 __device__ __forceinline__ VPiece<D> load_vpiece(const uint8_t *p)
 {
     VPiece<D> r;
     if constexpr (D == 256) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(p);
-        r.w[0] = x.x, r.w[1] = x.y;
+        const uint64_t x = *reinterpret_cast<const uint64_t *>(p);
+        r.w[0] = (uint32_t)x, r.w[1] = (uint32_t)(x >> 32);
     } else if constexpr (D == 128) {
         r.w[0] = *reinterpret_cast<const uint32_t *>(p);
     } else {
@@ -123,6 +214,22 @@ __device__ __forceinline__ VPiece<D> load_vpiece(const uint8_t *p)
     }
     return r;
 }
+// From LDS (as such: a read that only the optimiser knows to be one waits for every load to LDS on its way).
+template <int D>
+__device__ __forceinline__ VPiece<D> read_vpiece(const uint8_t *p)
+{
+    VPiece<D> r;
+    if constexpr (D == 256) {
+        const uint64_t x = *(const MROPE_LDS uint64_t *)p;
+        r.w[0] = (uint32_t)x, r.w[1] = (uint32_t)(x >> 32);
+    } else if constexpr (D == 128) {
+        r.w[0] = *(const MROPE_LDS uint32_t *)p;
+    } else {
+        r.w[0] = *(const MROPE_LDS uint16_t *)p;
+    }
+    return r;
+}
+#undef MROPE_LDS
 
 // Workgroups of a compute unit that run at once: LDS holds one of 256 dims, and the registers two waves a SIMD.
 constexpr int tree_resident(int io, int head_dim, int nb) { return head_dim == 64 && io != kIoF32 && nb == 1 ? 2 : 1; }
@@ -155,31 +262,25 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int col = lane & 31, half = lane >> 5;
     const int share = wave % kShares, row0 = wave / kShares * 32 * NB;  // the wave's tokens, its first row of the tile
-    const int g = a.nq / kv.nk, kvh = blockIdx.y;
+    const int g = a.nq / kv.nk;
 
-    Cut cut = {0, 0, 0, 1};
-    int32_t z = 0;
+    Cut cut;
     Tile tl;
-    if (p.max_cut == 0) {  // tables of one chunk
-        if (!find_tile<R>(a, g, blockIdx.x, lane, tl)) return;
-    } else {
-        CutList *list = static_cast<CutList *>(a.workspace);
-        int32_t rank, n_cut;
-        const bool found = find_chunk<R, true>(a, g, blockIdx.x, p.budget, lane, cut, z, rank, n_cut);
-        if (blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) list->n = min(n_cut, p.max_cut);
-        if (!found) return;
-        if (cut.n > 1) {
-            if (rank >= p.max_cut || cut.slot + cut.n > p.max_slots) return;  // (not for offsets that grow)
-            if (z == 0 && kvh == 0 && threadIdx.x == 0) list->cut[rank] = cut;
-        }
-        make_tile<R>(a, g, cut.s, cut.tile, tl);
+    int32_t z, rank, n_cut, kvh;
+    const bool found = find_fit<R, 32 * kShares>(a, g, blockIdx.x, p.budget, lane, cut, z, rank, n_cut, kvh, tl);
+    CutList *list = static_cast<CutList *>(a.workspace);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.max_cut) list->n = min(n_cut, p.max_cut);
+    if (!found) return;
+    if (cut.n > 1) {
+        if (rank >= p.max_cut || cut.slot + cut.n > p.max_slots) return;  // (not for offsets that grow)
+        if (z == 0 && kvh == 0 && threadIdx.x == 0) list->cut[rank] = cut;
     }
     const int n_rows = min(R, tl.rows - tl.row0);
     const int32_t len = tl.rows / g;
     const int32_t seen = __builtin_amdgcn_readfirstlane((int32_t)tl.seen);
     const int32_t past = __builtin_amdgcn_readfirstlane((int32_t)tl.past);  // (>= -2^31: ctx >= 0)
     const int32_t open = min(max(past, 0), seen);                     // every row sees the positions before this
-    const int32_t chunk = chunk_of(seen, cut.n, kFewUnit);
+    const int32_t chunk = chunk_of(seen, cut.n, 32 * kShares);
     const int32_t c0 = __builtin_amdgcn_readfirstlane((int32_t)min((int64_t)z * chunk, (int64_t)seen));
     const int32_t c1 = __builtin_amdgcn_readfirstlane(min(c0 + chunk, seen));
 
@@ -188,25 +289,27 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
     // Blocks of 32 tokens: this wave's i-th begins at c0 + (i kShares + share) * 32.  Pages of 32 of them at a time, those
     // of a sixteen of tokens a lane.
     const int32_t *table = kv.tables + tl.s * kv.table_stride;
+    int32_t tok_lane, page_lane;
     int64_t base;
     float ks_lane, vs_lane;
+    bool valid;
     uint64_t valid_mask;
-    auto look_up = [&](int i) {
-        base = 0;
-        ks_lane = vs_lane = 1.0f;
-        bool valid = false;
-        const int64_t tok = (int64_t)c0 + ((i + (lane >> 1)) * kShares + share) * 32 + (lane & 1) * 16;
-        if (tok < c1) {
-            const int32_t page = table[tok >> kv.bs_shift];
-            valid = page >= 0 && page < kv.num_blocks;
-            if (valid) {
-                ks_lane = kv.k_scale[(int64_t)page * kv.nk + kvh];
-                vs_lane = pow2(scale_exp_of(kv.v_scale[(int64_t)page * kv.nk + kvh]) - kVDown);  // (finite, whatever nobody sees)
-                base = page * kv.c_block;
-            }
-            base += (tok & (kv.block_size - 1)) * kv.c_tok + kvh * kv.c_head;
-        }
+    auto ask_pages = [&](int i) {
+        tok_lane = c0 + ((i + (lane >> 1)) * kShares + share) * 32 + (lane & 1) * 16;  // (at most 2^27 + 2^13)
+        page_lane = table[min(tok_lane, c1 - 1) >> kv.bs_shift];
+    };
+    auto use_pages = [&] {
+        valid = tok_lane < c1 && page_lane >= 0 && page_lane < kv.num_blocks;
+        const int64_t page = valid ? page_lane : 0;
+        ks_lane = kv.k_scale[page * kv.nk + kvh];
+        vs_lane = kv.v_scale[page * kv.nk + kvh];
+        base = page * kv.c_block + (tok_lane & (kv.block_size - 1)) * kv.c_tok + kvh * kv.c_head;
         valid_mask = __ballot(valid);
+    };
+    auto settle = [&] {
+        ks_lane = valid ? ks_lane : 1.0f;
+        vs_lane = valid ? pow2(scale_exp_of(vs_lane) - kVDown) : 1.0f;  // (finite, whatever nobody sees)
+        asm volatile("" : "+v"(ks_lane), "+v"(vs_lane));  // (they have come: no later wait is for them)
     };
     struct Info {  // of a block: scales and whether the page is there, by sixteens of tokens
         float ks0, ks1, vs0, vs1;
@@ -234,8 +337,7 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
                 to_lds16(cache + (b + (j * RI) % 16 * kv.c_tok), off[j % kPeriod], to + 1024 * j);
         }
     };
-    auto fetch_keys = [&](int i) {
-        if (i && (i & 31) == 0) look_up(i);
+    auto info = [&](int i) {
         const int at = 2 * (i & 31);
         Info x;
         x.ks0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks_lane), at));
@@ -243,18 +345,46 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
         x.vs0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs_lane), at));
         x.vs1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(vs_lane), at + 1));
         x.ok0 = (valid_mask >> at) & 1, x.ok1 = (valid_mask >> (at + 1)) & 1;
-        if (!kTogether || wave < kShares) fetch(i, kv.k, koff, ring[kTogether ? i & 1 : 0].k);
         return x;
     };
-    auto fetch_values = [&](int i) {
-        if (!kTogether || wave >= kShares) fetch(i, kv.v, voff, ring[kTogether ? i & 1 : 0].v);
+    auto fetch_keys = [&](int i) { fetch(i, kv.k, koff, ring[kTogether ? i & 1 : 0].k); };
+    auto fetch_values = [&](int i) { fetch(i, kv.v, voff, ring[kTogether ? i & 1 : 0].v); };
+    auto fetch_mine = [&](int i) {  // of two groups the first brings keys, the other values
+        if (wave < kShares) fetch_keys(i);
+        else fetch_values(i);
+    };
+    auto look_up = [&](int i) {
+        ask_pages(i);
+        use_pages();
+        settle();
     };
     const int n_all = (c1 - c0 + 31) / 32, n_mine = n_all > share ? (n_all - share + kShares - 1) / kShares : 0;
+    if (n_mine > 0) ask_pages(0);
+
+    // The queries (past the last row: that one again) are asked for while the pages' numbers are on their way.
+    constexpr int kQLoads = (NS + WAVES - 1) / WAVES;
+    decltype(load8<IO>(a.q, 0)) raw[NB * GROUPS][kQLoads];
+#pragma unroll
+    for (int nb = 0; nb < NB * GROUPS; ++nb) {
+        const int row = tl.row0 + min(nb * 32 + col, n_rows - 1);
+        const int64_t off = (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head + 16 * half;
+#pragma unroll
+        for (int i = 0; i < kQLoads; ++i) {
+            const int s = (i * WAVES + wave) % NS;
+            raw[nb][i] = load8<IO>(a.q, off + 32 * (s >> 1) + 8 * (s & 1));
+        }
+    }
     Info next{};
     if (n_mine > 0) {
-        look_up(0);
-        next = fetch_keys(0);
-        fetch_values(0);
+        use_pages();
+        if constexpr (kTogether) {
+            fetch_mine(0);
+        } else {
+            fetch_keys(0);
+            fetch_values(0);
+        }
+        settle();
+        next = info(0);
     }
 
     // the scores' factor: its sign goes to Q, and zero makes Q zero, so the largest score is the largest sum
@@ -262,35 +392,30 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
     const float sign = a.scale_log2 < 0.0f ? -1.0f : (a.scale_log2 > 0.0f ? 1.0f : 0.0f);
 
     // The queries: piece s of lane (col, half) is dims 32 * (s / 2) + 16 * half + 8 * (s % 2) .. + 7 of row col.
-    auto query_terms = [&](int r, int s, int h, u32x4 (&w)[QT]) {
-        float x[8] = {};
-        if (r < n_rows) {
-            const int row = tl.row0 + r;
-            unpack8<IO>(load8<IO>(a.q, (int64_t)(tl.t0 + row / g) * a.q_tok + (int64_t)(kvh * g + row % g) * a.q_head +
-                                           32 * (s >> 1) + 16 * h + 8 * (s & 1)), x);
-        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= sign;
+    for (int nb = 0; nb < NB * GROUPS; ++nb)
 #pragma unroll
-        for (int t = 0; t < QT; ++t)
+        for (int i = 0; i < kQLoads; ++i) {
+            float x[8];
+            unpack8<IO>(raw[nb][i], x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[t][i] = pack16x2<IO == kIoF16 ? kIoF16 : kIoBF16>(x[2 * i], x[2 * i + 1]);
-                if (t + 1 < QT) {
-                    float lo, hi;
-                    unpack16x2<kIoBF16>(w[t][i], lo, hi);
-                    x[2 * i] -= lo;
-                    x[2 * i + 1] -= hi;
+            for (int e = 0; e < 8; ++e) x[e] *= sign;
+            u32x4 w[QT];
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[t][e] = pack16x2<IO == kIoF16 ? kIoF16 : kIoBF16>(x[2 * e], x[2 * e + 1]);
+                    if (t + 1 < QT) {
+                        float lo, hi;
+                        unpack16x2<kIoBF16>(w[t][e], lo, hi);
+                        x[2 * e] -= lo;
+                        x[2 * e + 1] -= hi;
+                    }
                 }
-            }
-    };
-    for (int e = threadIdx.x; e < NB * GROUPS * NS * 64; e += 64 * WAVES) {
-        const int el = e & 63, s = (e >> 6) % NS, nb = (e >> 6) / NS;
-        u32x4 w[QT];
-        query_terms(nb * 32 + (el & 31), s, el >> 5, w);
 #pragma unroll
-        for (int t = 0; t < QT; ++t) lds.q[nb][t][s][el] = w[t];
-    }
+            for (int t = 0; t < QT; ++t) lds.q[nb][t][(i * WAVES + wave) % NS][lane] = w[t];  // (by two waves the same, of few pieces)
+        }
     __syncthreads();
 
     int32_t itok[NB];  // the query token of this lane's row of each thirty-two
@@ -347,8 +472,9 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
         // its keys have come (its values, NI instructions, may be on their way)
         if constexpr (!kTogether) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NI) : "memory");
         else if (more) {
-            next = fetch_keys(it + 1);
-            fetch_values(it + 1);
+            if ((it + 1) % 32 == 0) look_up(it + 1);
+            fetch_mine(it + 1);
+            next = info(it + 1);
         }
 #pragma unroll
         for (int k = 0; k < kKeysAhead; ++k) kp[k] = key_piece(k);
@@ -377,7 +503,9 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
         }
         if (!kTogether && more) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the keys have been read
-            next = fetch_keys(it + 1);
+            if ((it + 1) % 32 == 0) look_up(it + 1);
+            fetch_keys(it + 1);
+            next = info(it + 1);
         }
 
         edge = tok0 + 32 > open || !now.ok0 || !now.ok1;
@@ -442,7 +570,7 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                vp[u][j] = load_vpiece<D>(blk.v + value_row_of<D>(16 * u + 8 * (j >> 2) + 4 * half + (j & 3)) * D + col * NO);
+                vp[u][j] = read_vpiece<D>(blk.v + value_row_of<D>(16 * u + 8 * (j >> 2) + 4 * half + (j & 3)) * D + col * NO);
         // A NaN that some rows see and others do not, or that nobody sees, must not reach the product: the product
         // goes on without it, and the rows that see it are told at the end.
         if (edge) {
@@ -503,20 +631,22 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
         // scores.  The first group brings keys, the second values, both at the start of their scores: a block two
         // barriers before anyone wants it, to where the block before last was, which nobody reads any more.
         static_assert(GROUPS == 2, "two groups take turns");
+        auto meet = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };  // (what was read from LDS is here)
         const int n_loop = (n_all + kShares - 1) / kShares;
-        if (wave >= kShares) __syncthreads();
+        // (barriers of their own: __syncthreads would wait for the codes on their way at each)
+        if (wave >= kShares) meet();
         for (int it = 0; it < n_mine; ++it) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what this wave asked for has come
-            __syncthreads();
+            meet();
             scores(it, it + 1 < n_mine);
-            __syncthreads();
+            meet();
             product(it, it + 1 < n_mine);
         }
         if (n_mine < n_loop) {  // (a last round in which this wave has no block)
-            __syncthreads();
-            __syncthreads();
+            meet();
+            meet();
         }
-        if (wave < kShares) __syncthreads();
+        if (wave < kShares) meet();
     }
 
     if (__any(nan != 0)) {  // (rare) the blocks with a mask again: the rows that see a NaN have it in these dims
@@ -579,11 +709,13 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
                           ((int64_t)(cut.slot + z) * kv.nk + kvh);
     constexpr int kSlice = TreeLds<IO, D, NB, GROUPS, WAVES>::kSlice, kSlices = 32 / kSlice;
 #pragma unroll
-    for (int w = 0; w < NB * kSlices * GROUPS; ++w) {
-        const int n = w / kSlices % NB, slice = w % kSlices, first = w / (kSlices * NB) * 32 * NB + n * 32 + slice * kSlice;
+    for (int n = 0; n < NB; ++n)
+#pragma unroll 1
+    for (int w = 0; w < kSlices * GROUPS; ++w) {  // (rolled: what runs once is bound by the fetch of its code)
+        const int slice = w % kSlices, first = (w / kSlices * NB + n) * 32 + slice * kSlice;
         if (first >= n_rows) continue;
-        if (w) __syncthreads();  // the rows before have been read
-        if (wave / kShares == w / (kSlices * NB) && col / kSlice == slice) {
+        if (n || w) __syncthreads();  // the rows before have been read
+        if (wave / kShares == w / kSlices && col / kSlice == slice) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 float *dst = &lds.o[share][col % kSlice][(8 * (e >> 2) + 4 * half + (e & 3)) * NO];
@@ -642,6 +774,7 @@ struct TreePlan {
 struct Shape {
     int nb, groups, waves;  // (see the kernel)
     constexpr int rows() const { return 32 * nb * groups; }
+    constexpr int unit() const { return 32 * waves / groups; }  // a chunk's tokens are a multiple of
 };
 
 // fp32 queries take three times the room in LDS: tiles of 32 rows, and of 256 dims four waves.
@@ -660,7 +793,7 @@ TreePlan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int
     const int64_t seq_rows = (n_tokens * g + n_seqs - 1) / n_seqs;
     p.wide = seq_rows > 32 && io != kIoF32;
     const Shape shape = shape_of(io, head_dim, p.wide);
-    const int64_t rows = shape.rows(), most = (cap + kFewUnit - 1) / kFewUnit;
+    const int64_t rows = shape.rows(), most = (cap + shape.unit() - 1) / shape.unit();
     p.tiles = n_tokens * g / rows + n_seqs;
     p.few.budget = std::max(1, 256 * tree_resident(io, head_dim, shape.nb) / nk);
     p.grid = std::min(std::max<int64_t>(p.tiles, p.few.budget), p.tiles * most);
@@ -676,7 +809,8 @@ template <int IO, int D, bool WIDE>
 hipError_t launch_tree_shape(const AttendTree &a, const TreePlan &p, hipStream_t stream)
 {
     constexpr Shape S = shape_of(IO, D, WIDE);
-    attend_tree_kernel<IO, D, S.nb, S.groups, S.waves><<<dim3((unsigned)p.grid, a.kv.nk), 64 * S.waves, 0, stream>>>(a, p.few);
+    const unsigned grid = (unsigned)((p.grid * a.kv.nk + 7) / 8 * 8);  // as many for each XCD
+    attend_tree_kernel<IO, D, S.nb, S.groups, S.waves><<<grid, 64 * S.waves, 0, stream>>>(a, p.few);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.few.max_cut == 0) return e;
     // (as many chunks a tile as the budget has for the tiles there may be, or some more)

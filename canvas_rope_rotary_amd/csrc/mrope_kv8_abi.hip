@@ -184,10 +184,11 @@ mrope_status check_attend(const void *q, int64_t q_tok_stride, int64_t q_head_st
                    n_kv_heads, head_dim, block_tables, table_stride, table_width, n_seqs);
     if (st != MROPE_OK) return st;
     if (!aligned(lse, 4)) return fail(MROPE_ERR_ALIGN, "lse must be 4-byte aligned");
-    // a tile has 256 threads, and at least 4 rows, or 128 in a grid of all KV heads
+    // a tile has 256 threads, and at least 4 rows, or 128 in a grid of all KV heads (a tree's: 512 and 32)
     const int64_t group = n_q_heads / n_kv_heads;
     if ((n_tokens * ((group + 3) / 4) + n_seqs + 1024) * 256 > kMaxGridThreads ||
-        (n_tokens * group / 128 + n_seqs) * n_kv_heads * 256 > kMaxGridThreads)
+        (n_tokens * group / 128 + n_seqs) * n_kv_heads * 256 > kMaxGridThreads ||
+        (tree && (n_tokens * group / 32 + n_seqs + 1024) * n_kv_heads * 512 > kMaxGridThreads))
         return fail(MROPE_ERR_ARG, "too many query rows (%lld tokens, %d heads a KV head)", (long long)n_tokens, (int)group);
     if ((int64_t)table_width * block_size > kMaxContext)
         return fail(MROPE_ERR_ARG, "block_tables: at most 2^27 positions a sequence (got %lld)", (long long)table_width * block_size);
