@@ -3,22 +3,30 @@
 //   out[t, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q[t, h] . k_j - max),
 //
 // over the positions j that query token i (of len) of a sequence of ctx positions sees: those before ctx - len,
-// and ctx - len + b for the bits b that are set in its row of the mask.  Rows, tiles, chunks of contexts and the
-// join are those of mrope_attend.h; a row is a (token, head of the group) pair, row = i * g + head.
+// and ctx - len + b for the bits b that are set in its row of the mask.  Tiles, chunks of contexts and the join are those of
+// mrope_attend.h; a row is a (token, head of the group) pair, row = i * g + head.
 //
-// One workgroup: 32 or 64 rows against a chunk of the context, its four waves taking 32 tokens in turn, each
-// with all the rows.  S^T = K Q^T (32 x 32 x 16): a lane ends with the scores of one row of each thirty-two (its
-// column) for sixteen of the tokens, keys 8a + 4h + b, a, b < 4, of lane half h; O^T = V^T P^T takes sixteen tokens a step
-// and each lane's operand is what it has there, if V's comes in the same order.  So nothing moves between lanes
-// but for the maximum, and the waves meet only once, at the end.  A block's K and V are decoded once for all rows
-// (codes are exact in 16 bits, V with its scale).  P is taken in two bf16 terms for the 16-bit types and three for fp32,
-// fp32 queries in three (each the bf16 nearest to what the terms before it leave).
+// One workgroup: 32 or 64 rows against a chunk of the context, eight waves (four for fp32 heads of 256), two a SIMD, that
+// take 32 tokens each in turn with thirty-two rows, or all 64 where the registers hold them (heads of up to 128).
+// S^T = K Q^T (32 x 32 x 16): a lane ends with the scores of one row of each thirty-two (its column) for sixteen of the
+// tokens, keys 8a + 4h + b, a, b < 4, of lane half h; O^T = V^T P^T takes sixteen tokens a step and each lane's operand is
+// what it has there, if V's comes in the same order.  So nothing moves between lanes but for the maximum, and the parts of
+// waves with other tokens meet only once, at the end.  Codes are exact in 16 bits, V with its scale.  P is taken in two bf16
+// terms for the 16-bit types (2^-17, as the other kernels over this cache do) and three for fp32, fp32 queries in three (each
+// the bf16 nearest to what the terms before it leave).
 //
-// Codes come to LDS by loads that pass no register, a block ahead, into a ring of the wave's own: no wave waits
-// for another.  The queries of 64 rows wait in LDS, in the order of the instruction's operand; those of 32 rows
-// stay in registers.
+// Codes come to LDS by loads that pass no register, a block ahead: into a ring of the wave's own, so no wave waits for
+// another, or into one that two waves with other rows share, so a block is brought once for 64 rows.  The queries wait in
+// LDS in the order of the instruction's operand.
 //
 // Only blocks that reach past ctx - len, or into a page that is not there, look at the mask.
+//
+// Measured, heads of 256 in bf16, 8 of 2 KV heads: 64 trees of 32 tokens at 4,096 positions 122 us and the join, 103 GFLOP
+// with P's second term, 0.84 PFLOP/s; the matrix instructions are busy for 47 % of the time and the others, decoding and
+// the softmax, for as much: on the two waves of a SIMD the sum of both is 95 % of the cycles.  8 trees of 16 at 32,000
+// positions: 72 us and the join's 6, 263 MB of codes (3.7 TB/s).  A call of one tree at a short context is a chain of
+// waits, 12 us: 2 to find the chunk, 3 for the page's number, then its codes and scales, 1 for the queries, 2 for a block,
+// 4 for the parts to meet, most of them for code that comes for the first time.
 #include <algorithm>
 
 #include "mrope_attend.h"
@@ -57,6 +65,9 @@ __device__ __forceinline__ uint32_t key_pair(uint32_t u, float scale)
     else return bf16_pair<HI>(u, scale);
 }
 
+// Workgroups of a compute unit that run at once: registers hold two waves a SIMD but for 32 rows of 64 dims.
+constexpr int tree_resident(int io, int head_dim, int nb) { return head_dim == 64 && io != kIoF32 && nb == 1 ? 2 : 1; }
+
 // Running sum over the lanes: within sixteens, then a sixteen's last to those behind it.
 __device__ __forceinline__ int32_t running(int32_t x)
 {
@@ -69,12 +80,28 @@ __device__ __forceinline__ int32_t running(int32_t x)
     return x;
 }
 
+// The largest of the lanes' (none of them negative).
+__device__ __forceinline__ int32_t largest(int32_t x)
+{
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
 // The work of workgroup `id`: a chunk of a tile, of chunks that are as long as one another and fit those that run at once:
-// at most `budget` a KV head, or the tiles, none of them cut.  A chunk is `unit` times U tokens, and a tile adds less than one
-// chunk to its share of the sum, so what the tiles leave of the budget is shared.  `z` is the chunk's place in its tile, `rank`
-// that of the tile in the list of cut ones.  The chunks of all heads in order, an eighth to each XCD (id % 8): tiles of the same
-// context and heads of the same pages meet in its L2.
-template <int R, int U>
+// at most `budget` a KV head, or the tiles, none of them cut.  A chunk is `unit` times U tokens: the least that fits, which
+// lies between the sum's share and, as a tile adds less than one chunk to its share, that of what the tiles leave of the budget
+// (more than 64 sequences, a second look at each for each trial, take the latter).  Tiles stay whole where the cut does not
+// shorten the longest by GAIN tokens, times the share of the budget that it takes, since parts are written and read again (16
+// trees of 32 at 1,000 positions, heads of 256: 26.3 us whole, 30.0 in two; 64 of 16 at 4,096 in tiles of 64 rows: 97.3 and
+// 80.3).  `z` is the chunk's place in its tile,
+// `rank` that of the tile in the list of cut ones.  The chunks of all heads in order, an eighth to each XCD (id % 8): tiles of
+// the same context and heads of the same pages meet in its L2.
+template <int R, int U, int GAIN>
 __device__ __forceinline__ bool find_fit(const AttendTree &a, int g, int32_t id, int32_t budget, int lane, Cut &c, int32_t &z,
                                          int32_t &rank, int32_t &n_cut, int32_t &kvh, Tile &t)
 {
@@ -88,25 +115,36 @@ __device__ __forceinline__ bool find_fit(const AttendTree &a, int g, int32_t id,
         tiles = (int32_t)(((int64_t)max(len, 0) * g + R - 1) / R);
         units = (seen + U - 1) / U;
     };
-    int32_t all = 0, total = 0;
+    int32_t all = 0, total = 0, longest = 0;
     for (int32_t s = lane; s - lane < a.n_seqs; s += 64) {
         read(s);
         all += tiles;
+        longest = max(longest, tiles ? units : 0);
         total += tiles * units;  // (matters where the tiles are fewer than the budget, and is below 2^31 then)
     }
     all = __builtin_amdgcn_readlane(running(all), 63);
     total = __builtin_amdgcn_readlane(running(total), 63);
     const int32_t left = budget - all;
-    const int32_t unit = left > 0 ? max((int32_t)(((uint32_t)total + left - 1) / (uint32_t)left), 1) : 1 << 30;
-    auto chunks_here = [&] { return max((int32_t)((uint32_t)(units + unit - 1) / (uint32_t)unit), 1); };
-    int32_t count = all;  // of chunks
-    if (left > 0) {
-        count = 0;
+    auto chunks_here = [&](int32_t unit) { return max((int32_t)((uint32_t)(units + unit - 1) / (uint32_t)unit), 1); };
+    auto count_of = [&](int32_t unit) {
+        int32_t c = 0;
         for (int32_t s = lane; s - lane < a.n_seqs; s += 64) {
             if (a.n_seqs > 64) read(s);
-            count += tiles * chunks_here();
+            c += tiles * chunks_here(unit);
         }
-        count = __builtin_amdgcn_readlane(running(count), 63);
+        return (int32_t)__builtin_amdgcn_readlane(running(c), 63);
+    };
+    int32_t unit = 1 << 30, count = all;  // of chunks
+    if (left > 0) {
+        unit = max((int32_t)(((uint32_t)total + left - 1) / (uint32_t)left), 1);
+        for (int32_t lo = max((int32_t)(((uint32_t)total + budget - 1) / (uint32_t)budget), 1); a.n_seqs <= 64 && lo < unit;) {
+            const int32_t mid = (lo + unit) >> 1;
+            if (count_of(mid) <= budget) unit = mid;
+            else lo = mid + 1;
+        }
+        count = count_of(unit);
+        const int32_t cut = largest(max(longest - unit, 0)) * U;  // (at most 2^27)
+        if ((int64_t)cut * budget < (int64_t)GAIN * count) unit = 1 << 30, count = all;
     }
     const int32_t nk = a.kv.nk, share = (int32_t)(((int64_t)count * nk + 7) / 8), v = id % 8 * share + id / 8;
     const bool mine = id / 8 < share && v < count * nk;
@@ -118,7 +156,7 @@ __device__ __forceinline__ bool find_fit(const AttendTree &a, int g, int32_t id,
     bool found = false;
     for (int32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
         if (a.n_seqs > 64) read(s0 + lane);
-        const int32_t n = chunks_here();
+        const int32_t n = chunks_here(unit);
         const int32_t own = tiles * n, own_cut = n > 1 ? tiles : 0;
         const int32_t up = running(own), up_cut = running(own_cut), up_slots = running(n > 1 ? own : 0);
         if (!found && base.all + __builtin_amdgcn_readlane(up, 63) > w) {
@@ -231,9 +269,6 @@ __device__ __forceinline__ VPiece<D> read_vpiece(const uint8_t *p)
 }
 #undef MROPE_LDS
 
-// Workgroups of a compute unit that run at once: LDS holds one of 256 dims, and the registers two waves a SIMD.
-constexpr int tree_resident(int io, int head_dim, int nb) { return head_dim == 64 && io != kIoF32 && nb == 1 ? 2 : 1; }
-
 // The largest of three (of the others where one is NaN), without the canonicalisation that fmaxf costs.
 __device__ __forceinline__ float max3(float x, float y, float z)
 {
@@ -267,7 +302,7 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
     Cut cut;
     Tile tl;
     int32_t z, rank, n_cut, kvh;
-    const bool found = find_fit<R, 32 * kShares>(a, g, blockIdx.x, p.budget, lane, cut, z, rank, n_cut, kvh, tl);
+    const bool found = find_fit<R, 32 * kShares, (D == 256 ? 768 : 1536) * tree_resident(IO, D, NB)>(a, g, blockIdx.x, p.budget, lane, cut, z, rank, n_cut, kvh, tl);
     CutList *list = static_cast<CutList *>(a.workspace);
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.max_cut) list->n = min(n_cut, p.max_cut);
     if (!found) return;
@@ -625,28 +660,17 @@ __global__ __launch_bounds__(64 * WAVES, tree_resident(IO, D, NB) * WAVES / 4) v
             product(it, it + 1 < n_mine);
         }
     } else {
-        // The two groups take turns: while one is at a block's scores and softmax, the other is at a product, so a SIMD's
-        // two waves want the matrix unit and the vector unit at different times.  Between two barriers the first group takes
-        // block i's scores while the second takes block i - 1's product, then block i's product while the second takes its
-        // scores.  The first group brings keys, the second values, both at the start of their scores: a block two
-        // barriers before anyone wants it, to where the block before last was, which nobody reads any more.
-        static_assert(GROUPS == 2, "two groups take turns");
-        auto meet = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };  // (what was read from LDS is here)
-        const int n_loop = (n_all + kShares - 1) / kShares;
-        // (barriers of their own: __syncthreads would wait for the codes on their way at each)
-        if (wave >= kShares) meet();
-        for (int it = 0; it < n_mine; ++it) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what this wave asked for has come
-            meet();
-            scores(it, it + 1 < n_mine);
-            meet();
-            product(it, it + 1 < n_mine);
+        // The first group brings a block's keys, the second its values, while the block before is at work, to where the one
+        // before that was: its readers have passed the barrier since.  (A barrier that leaves codes on their way, as
+        // __syncthreads does not.)
+        static_assert(GROUPS == 2, "two groups share a block");
+        for (int it = 0; it < (n_all + kShares - 1) / kShares; ++it) {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // what was asked for has come, what was read too
+            if (it < n_mine) {
+                scores(it, it + 1 < n_mine);
+                product(it, it + 1 < n_mine);
+            }
         }
-        if (n_mine < n_loop) {  // (a last round in which this wave has no block)
-            meet();
-            meet();
-        }
-        if (wave < kShares) meet();
     }
 
     if (__any(nan != 0)) {  // (rare) the blocks with a mask again: the rows that see a NaN have it in these dims
@@ -777,7 +801,9 @@ struct Shape {
     constexpr int unit() const { return 32 * waves / groups; }  // a chunk's tokens are a multiple of
 };
 
-// fp32 queries take three times the room in LDS: tiles of 32 rows, and of 256 dims four waves.
+// fp32 queries take three times the room in LDS: tiles of 32 rows, and of 256 dims four waves.  64 rows of 256 dims are two
+// waves' (a wave's registers hold 32), of fewer dims one wave's: for 128 dims 70.9 us against two waves' 81.9 (64 trees of
+// 32 at 4,096 positions), for 64 54.6 and 84.0.
 constexpr Shape shape_of(int io, int head_dim, bool wide)
 {
     if (io == kIoF32) return {1, 1, head_dim == 256 ? 4 : 8};
@@ -791,7 +817,11 @@ TreePlan make_plan(int64_t n_tokens, int32_t n_seqs, int32_t nq, int32_t nk, int
     TreePlan p{};
     const int64_t g = nq / nk, cap = std::max<int64_t>(1, (int64_t)table_width * block_size);
     const int64_t seq_rows = (n_tokens * g + n_seqs - 1) / n_seqs;
-    p.wide = seq_rows > 32 && io != kIoF32;
+    // Tiles of 64 rows decode a block for twice the rows, tiles of 32 spread further: narrow as long as all of them run at once
+    // (us, narrow and wide.  Fewer: 3 trees of 250 at 2,047 positions 41.7 and 51.0, 64 of 16 at 4,096 80.4 and 83.3, in heads of
+    // 128 27.9 and 38.8, 47.5 and 52.3, of 64 22.5 and 29.9, 32.9 and 39.2.  More: 64 of 32 at 4,096 136.3 and 126.0, 256 of 16 at
+    // 1,000 116.5 and 91.9, in heads of 128 83.1 and 73.4, 75.3 and 61.5, of 64 50.1 and 47.6, but 41.7 and 45.0).
+    p.wide = n_seqs * ((seq_rows + 31) / 32) * nk > 256 && io != kIoF32;
     const Shape shape = shape_of(io, head_dim, p.wide);
     const int64_t rows = shape.rows(), most = (cap + shape.unit() - 1) / shape.unit();
     p.tiles = n_tokens * g / rows + n_seqs;
@@ -813,7 +843,8 @@ hipError_t launch_tree_shape(const AttendTree &a, const TreePlan &p, hipStream_t
     attend_tree_kernel<IO, D, S.nb, S.groups, S.waves><<<grid, 64 * S.waves, 0, stream>>>(a, p.few);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.few.max_cut == 0) return e;
-    // (as many chunks a tile as the budget has for the tiles there may be, or some more)
+    // Waves a row of the join by the chunks a tile may have (us, eight and two waves: one tree of 8 at 30,000 positions 29.0
+    // and 43.2, two of 16 at 16,000 29.5 and 36.8; 8 of 16 at 32,000 80.5 and 79.4, 16 of 16 at 8,000 55.9 and 50.8).
     const unsigned tiles = (unsigned)p.few.max_cut;
     if (p.few.max_slots > kJoinMany * p.few.max_cut)
         attend_join_kernel<IO, D, S.rows(), 1><<<dim3(tiles, a.kv.nk, S.rows()), kJoinThreads, 0, stream>>>(a, 0, p.few.max_cut);
