@@ -459,6 +459,8 @@ mrope_status mrope_planes_tree(const int32_t *parents, int64_t n_tokens, const i
  * the sequence whose bit is set in
  * mask       [n_tokens][mask_words] uint64 (mrope_planes_tree's, or any other: a token need not see itself, or
  *            may see later ones).  Tokens without a bit are not seen.  mask_words 1..64.
+ * cache_tok_stride is below 2^28, and (n_tokens * n_q_heads / n_kv_heads / 32 + n_seqs + 1024) * n_kv_heads at most
+ * 2^23 (tiles of 32 rows of all sequences and KV heads).
  * ------------------------------------------------------------------------------------------- */
 size_t mrope_attend_tree_kv8_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
                                              int32_t head_dim, int32_t dtype, int32_t table_width, int32_t block_size);
