@@ -13,7 +13,9 @@
 // parts over workgroups.  Every workgroup of a sequence does the walk for itself (tests of single elements, fetched
 // side by side for all tokens), so nothing waits for another workgroup.  The last launch finds the part and the
 // element; walks that the rounds did not end it ends by itself, one workgroup a sequence.
-// Bound: the rows' bytes, and latency where sequences are few.
+// Bound: where sequences are few, latency (tokens, their probabilities, the walk, the row: 7.4 us for a round of one chain of
+// six over 248,094 ids, 3.6 for the last launch; 64 trees of 32 in bf16 16.4 and 4.7 for 32 MB); where they are many, the
+// conversion and addition of each element in 64 bits (2,000 rows of fp16: 992 MB in 267 us).
 #include <algorithm>
 #include <cmath>
 
@@ -300,7 +302,7 @@ __device__ double block_scan(double x, double &all, Shared &sh)
 template <int IO>
 __device__ void row_sums(const Verify &a, const Seq &sq, const Tree &t, const Walk &w, int32_t first, int32_t end, double *sums)
 {
-    constexpr int kAhead = 3;
+    constexpr int kAhead = 3;  // (64 trees of 32 in bf16: 23.1 us a call, with five 24.0, eight 26.4)
     const int lane = threadIdx.x & 63;
     const Gone gone(a, w, lane, [&](int32_t i) { return t.parent[i] == w.node ? t.id[i] : -1; });
     const int32_t from = first + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
