@@ -15,7 +15,7 @@
 // element; walks that the rounds did not end it ends by itself, one workgroup a sequence.
 // Bound: where sequences are few, latency (tokens, their probabilities, the walk, the row: 7.4 us for a round of one chain of
 // six over 248,094 ids, 3.6 for the last launch; 64 trees of 32 in bf16 16.4 and 4.7 for 32 MB); where they are many, the
-// conversion and addition of each element in 64 bits (2,000 rows of fp16: 992 MB in 225 us).
+// conversion and addition of each element in 64 bits (2,000 rows of fp16: 992 MB in 267 us).
 #include <algorithm>
 #include <cmath>
 
@@ -32,9 +32,7 @@ constexpr int kReads = kWaves, kSum = kRead * kReads;  // reads, and elements, o
 // A probability: what is not a positive number counts as 0.
 __device__ __forceinline__ double prob(float x)
 {
-    float y = __builtin_amdgcn_classf(x, 0x180) ? x : 0.0f;  // (positive and subnormal, positive and normal)
-    asm("" : "+v"(y));  // (chosen before it is widened: one register to choose, not two)
-    return y;
+    return __builtin_amdgcn_classf(x, 0x180) ? x : 0.0f;  // (positive and subnormal, positive and normal)
 }
 
 template <int IO>
