@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
 
 typedef float kv8_f32x2 __attribute__((ext_vector_type(2)));
 
-// Four e4m3 bytes times f (a power of two <= 1), rounded to e4m3 again.
+// Four e4m3 bytes times f, rounded to e4m3 again (f: a power of two that takes none of them past 448).
 __device__ __forceinline__ uint32_t shift_e4m3(uint32_t u, float f)
 {
     const kv8_f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)u, false);

@@ -166,7 +166,9 @@ __global__ __launch_bounds__(256) void keep_kernel(Keep a, KeepLayers layers)
 #pragma unroll
         for (int k = 0; k < NL; ++k) {
             if (!mine[k] || (!moved[k] && es[k] == e)) continue;
-            const float f = pow2(max(es[k] - e, -126));
+            // (a number other than 0 is 2^-9 of its scale at least, so its page's is no less than 2^-17 of it; a row of zeros
+            // may come from any)
+            const float f = pow2(min(max(es[k] - e, -126), 17));
 #pragma unroll
             for (int w = 0; w < 4; ++w) x[k][w] = shift_e4m3(x[k][w], f);
             *reinterpret_cast<u32x4 *>(to + (k * RPL + sub) * kv.c_tok) = x[k];
