@@ -109,6 +109,20 @@ __device__ __forceinline__ bool any_nan(uint32_t u)
     return (x & 0x80808080u) != 0;
 }
 
+// The largest of three (of the others where one is NaN): one instruction, without the canonicalisation that fmaxf costs, and
+// one that the compiler knows to read a matrix instruction's result, which needs wait states.
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    return __builtin_elementwise_maximumnum(__builtin_elementwise_maximumnum(x, y), z);
+}
+
+// The larger of a lane's and its counterpart's in the other half of the wave.
+__device__ __forceinline__ float max_halves(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return max3(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[1]));
+}
+
 template <int D>
 struct VRow {
     uint32_t w[D / 64];  // D/16 bytes

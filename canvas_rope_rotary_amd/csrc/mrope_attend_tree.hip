@@ -269,21 +269,6 @@ __device__ __forceinline__ VPiece<D> read_vpiece(const uint8_t *p)
 }
 #undef MROPE_LDS
 
-// The largest of three (of the others where one is NaN), without the canonicalisation that fmaxf costs.
-__device__ __forceinline__ float max3(float x, float y, float z)
-{
-    float r;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
-    return r;
-}
-
-// The larger of a lane's and its counterpart's in the other half of the wave.
-__device__ __forceinline__ float max_halves(float x)
-{
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return max3(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[1]));
-}
-
 // V's page scale (2^8 smaller) beside which the running maximum follows at once.
 constexpr float kLargeScale = 0x1p72f;
 
