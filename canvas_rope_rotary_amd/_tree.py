@@ -186,8 +186,8 @@ def keep_kv8(n_kept: torch.Tensor, path: torch.Tensor, cu_seqlens: torch.Tensor,
              block_tables: torch.Tensor, caches) -> None:
     """Move the cache rows of accepted paths together: of each sequence the row at position pos_offset +
     path[i] goes to pos_offset + i, for i < n_kept, in every layer's (k_cache, v_cache, k_scale, v_scale) of
-    `caches` (all of one shape and strides, at most MAX_LAYERS), under the scales that an append of these rows
-    would give their pages.  n_kept [n] and path [T] as verify_tree returns them; pos_offset [n] int32:
+    `caches` (all of one shape and strides, at most MAX_LAYERS; a cache that layers share is given once), under
+    the scales that an append of these rows would give their pages.  n_kept [n] and path [T] as verify_tree returns them; pos_offset [n] int32:
     the position of each sequence's token 0 (the context then is pos_offset + n_kept)."""
     caches = tuple(caches)
     if not caches:

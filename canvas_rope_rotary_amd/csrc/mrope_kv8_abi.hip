@@ -3,7 +3,6 @@
 #include <algorithm>
 #include <cmath>
 #include <numeric>
-#include <utility>
 
 #include "mrope_kv8.h"
 #include "mrope_pages.h"
@@ -47,19 +46,68 @@ mrope_status check_kv8(const void *k_cache, const void *v_cache, const float *k_
     return MROPE_OK;
 }
 
+struct Dim {
+    int64_t stride, extent;
+    bool operator<(const Dim &o) const { return stride < o.stride; }
+};
+
 // An append writes every row of a page from one workgroup and pages from many: rows must lie apart (by the
 // strides in ascending order each past all rows of those before it).
 mrope_status check_rows_apart(int64_t num_blocks, int64_t c_block, int32_t block_size, int64_t c_tok, int32_t nk, int64_t c_head,
                               int32_t head_dim)
 {
-    std::pair<int64_t, int64_t> dims[3] = {{c_block, num_blocks}, {c_tok, block_size}, {c_head, nk}};  // stride, extent
+    Dim dims[3] = {{c_block, num_blocks}, {c_tok, block_size}, {c_head, nk}};
     std::sort(dims, dims + 3);
     int64_t span = head_dim;
     for (const auto &d : dims) {
-        if (d.second <= 1) continue;
-        if (d.first < span) return fail(MROPE_ERR_ARG, "cache strides: rows overlap");
-        span += (d.second - 1) * d.first;
+        if (d.extent <= 1) continue;
+        if (d.stride < span) return fail(MROPE_ERR_ARG, "cache strides: rows overlap");
+        span += (d.extent - 1) * d.stride;
     }
+    return MROPE_OK;
+}
+
+// Whether a row of one cache comes within head_dim bytes of a row `d` bytes on in another's order: `n` strides in ascending
+// order, each past all rows of those before it, so the rows' indexes differ by d / stride or the number after it.
+bool rows_meet(const Dim *dims, int n, int64_t d, int32_t head_dim)
+{
+    if (n == 0) return d < head_dim && -d < head_dim;
+    const Dim &top = dims[n - 1];
+    const int64_t k = d >= 0 ? d / top.stride : -((-d + top.stride - 1) / top.stride);
+    for (int64_t i = k; i <= k + 1; ++i)
+        if (i < top.extent && -i < top.extent && rows_meet(dims, n - 1, d - i * top.stride, head_dim)) return true;
+    return false;
+}
+
+// Calls that write the caches of several layers at once do so from waves of their own for each cache and head: no
+// two caches (of one shape and strides, rows apart in each) may share a row, and no two of their scales memory.
+mrope_status check_layers_apart(const mrope_kv8_layer *layers, int32_t n_layers, int64_t num_blocks, int64_t c_block,
+                                int32_t block_size, int64_t c_tok, int32_t nk, int64_t c_head, int32_t head_dim)
+{
+    if (num_blocks == 0) return MROPE_OK;
+    const Dim all[3] = {{c_block, num_blocks}, {c_tok, block_size}, {c_head, nk}};
+    Dim dims[3];
+    int n_dims = 0;
+    uint64_t span = head_dim;
+    for (const auto &d : all)
+        if (d.extent > 1) dims[n_dims++] = d, span += (uint64_t)((d.extent - 1) * d.stride);
+    std::sort(dims, dims + n_dims);
+    uintptr_t codes[2 * MROPE_MAX_LAYERS], scales[2 * MROPE_MAX_LAYERS];
+    const int n = 2 * n_layers;
+    for (int i = 0; i < n; ++i) {
+        const mrope_kv8_layer &l = layers[i >> 1];
+        codes[i] = reinterpret_cast<uintptr_t>(i & 1 ? l.v_cache : l.k_cache);
+        scales[i] = reinterpret_cast<uintptr_t>(i & 1 ? l.v_scale : l.k_scale);
+    }
+    std::sort(codes, codes + n);
+    std::sort(scales, scales + n);
+    for (int i = 0; i < n; ++i)
+        for (int j = i + 1; j < n && codes[j] - codes[i] < span; ++j)
+            if (rows_meet(dims, n_dims, (int64_t)(codes[j] - codes[i]), head_dim))
+                return fail(MROPE_ERR_ARG, "caches of different layers, or K's and V's of one, share rows");
+    for (int i = 0; i + 1 < n; ++i)
+        if (scales[i + 1] - scales[i] < (uint64_t)num_blocks * nk * sizeof(float))
+            return fail(MROPE_ERR_ARG, "scales of different layers, or K's and V's of one, share memory");
     return MROPE_OK;
 }
 
@@ -506,6 +554,9 @@ mrope_status mrope_keep_kv8(const mrope_kv8_layer *layers, int32_t n_layers, int
     if (((int64_t)n_seqs * n_layers * 2 * n_kv_heads + 3) / 4 * 256 > kMaxGridThreads)
         return fail(MROPE_ERR_ARG, "too many sequences for the layers and heads (%d)", n_seqs);
     if (n_tokens == 0 || n_layers == 0) return MROPE_OK;
+    st = check_layers_apart(layers, n_layers, num_blocks, cache_block_stride, block_size, cache_tok_stride, n_kv_heads,
+                            cache_head_stride, head_dim);
+    if (st != MROPE_OK) return st;
     if (!n_kept || !path || !pos_offset) return fail(MROPE_ERR_ARG, "n_kept / path / pos_offset is NULL");
     Keep a{};
     a.n_kept = n_kept;

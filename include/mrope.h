@@ -510,7 +510,9 @@ mrope_status mrope_verify_tree(const void *target, int64_t target_stride, const 
 /* ---------------------------------------------------------------------------------------------
  * mrope_keep_kv8 -- move the cache rows of accepted paths together, in the caches of every layer.
  *
- * layers     [n_layers] (host array): the caches and scales of each layer, all of one shape and strides.
+ * layers     [n_layers] (host array): the caches and scales of each layer, all of one shape and strides.  No two of the
+ *            caches share a row and no two of the scales memory, K's and V's of one layer included (MROPE_ERR_ARG):
+ *            layers that use one cache between them give it once.
  * n_kept [n_seqs], path [n_tokens] int32: as mrope_verify_tree leaves them: of sequence s the i-th kept row is that of
  *            token path[cu_seqlens[s] + i], i < n_kept[s].  The entries ascend; the first that does not, or lies
  *            outside the tree, ends the list.

@@ -1,0 +1,96 @@
+"""CPU checks of what the calls for trees of drafted tokens refuse to write: memory that they would write twice, or read and
+write at once.  Nothing is launched."""
+import ctypes
+import itertools
+import random
+
+import pytest
+
+from test_tree_abi_cpu import A, ARG, BASE, lib  # noqa: F401  (lib: a fixture)
+
+
+# ---------------------------------------------------------------- keep --------------------------
+def keep(lib, layers, **kw):  # noqa: F811
+    """Status and message of a call whose last argument to be looked at, n_kept, is missing."""
+    a = {**BASE, "nkept": None, **kw}
+    flat = [p for layer in layers for p in layer]
+    arr = (ctypes.c_uint64 * len(flat))(*flat)
+    st = lib.mrope_keep_kv8(arr, len(layers), a["nk"], a["hd"], a["bs"], a["nb"], a["cb"], a["ct"], a["ch"], a["nkept"], a["path"], a["n"],
+                            a["cu"], a["ns"], a["pos"], a["tab"], a["ts"], a["tw"], None)
+    return st, lib.mrope_last_error().decode()
+
+
+def apart(result):
+    assert result[0] == ARG and ("share" in result[1] or "n_kept" in result[1]), result
+    return "n_kept" in result[1]
+
+
+CACHE, SCALE = 64 * 8192, 64 * 2 * 4  # bytes of a cache and its scales in BASE
+
+
+def layers_of(n):
+    return [[A + 2 * i * CACHE, A + (2 * i + 1) * CACHE, (1 << 40) + 2 * i * SCALE, (1 << 40) + (2 * i + 1) * SCALE] for i in range(n)]
+
+
+@pytest.mark.parametrize("n", [1, 2, 6, 64])
+def test_keep_takes_caches_side_by_side(lib, n):  # noqa: F811
+    assert apart(keep(lib, layers_of(n)))
+
+
+@pytest.mark.parametrize("n", [2, 64])
+@pytest.mark.parametrize("what", [0, 1, 2, 3])
+def test_keep_refuses_a_layer_twice(lib, n, what):  # noqa: F811
+    layers = layers_of(n)
+    layers[n - 1][what] = layers[0][what]
+    assert not apart(keep(lib, layers))
+    layers = layers_of(n)
+    layers[n - 1][what ^ 1] = layers[0][what]  # K in V's place
+    assert not apart(keep(lib, layers))
+
+
+@pytest.mark.parametrize("what", [0, 2])
+def test_keep_refuses_k_and_v_in_one(lib, what):  # noqa: F811
+    layers = layers_of(1)
+    layers[0][what + 1] = layers[0][what]
+    assert not apart(keep(lib, layers))
+
+
+@pytest.mark.parametrize("by,fine", [(CACHE, True), (CACHE - 16, False), (16, False), (8192, False)])
+def test_keep_caches_that_overlap_in_part(lib, by, fine):  # noqa: F811
+    layers = layers_of(1)
+    layers[0][1] = layers[0][0] + by
+    assert apart(keep(lib, layers)) is fine
+
+
+@pytest.mark.parametrize("by,fine", [(SCALE, True), (SCALE - 4, False), (4, False)])
+def test_keep_scales_that_overlap_in_part(lib, by, fine):  # noqa: F811
+    layers = layers_of(1)
+    layers[0][3] = layers[0][2] + by
+    assert apart(keep(lib, layers)) is fine
+
+
+def test_keep_empty_pool(lib):  # noqa: F811
+    assert apart(keep(lib, [[0, 0, 0, 0]] * 2, nb=0))
+
+
+def test_keep_layers_by_every_row(lib):  # noqa: F811
+    """Two caches with their dimensions in any order and gaps, at every distance of some rows: refused exactly where a row of one
+    touches a row of the other."""
+    rng = random.Random(5)
+    seen = [0, 0]
+    for turn in range(400):
+        nk, nb, bs, D = rng.randrange(1, 4), rng.randrange(1, 4), 16, 64
+        strides, span = {}, D
+        for name, extent in rng.sample([("ch", nk), ("ct", bs), ("cb", nb)], 3):
+            strides[name] = max(-(-span // 16) * 16 + 16 * rng.choice([0, 0, 1, 5, 40]), D)
+            if extent > 1:
+                span += (extent - 1) * strides[name]
+        d = 16 * rng.randrange(0, span // 16 + 3)
+        rows = [b * strides["cb"] + t * strides["ct"] + h * strides["ch"] for b, t, h in itertools.product(range(nb), range(bs), range(nk))]
+        taken = {r + x for r in rows for x in range(0, D, 16)}
+        fine = not any(r + d + x in taken for r in rows for x in range(0, D, 16))
+        pair = [A, A + d] if turn % 2 else [A + d, A]
+        got = keep(lib, [[*pair, 1 << 40, 1 << 41]], nk=nk, nb=nb, bs=bs, hd=D, ts=8, **strides)
+        assert apart(got) is fine, (nk, nb, strides, d)
+        seen[fine] += 1
+    assert min(seen) > 50
