@@ -285,6 +285,41 @@ mrope_status check_trees(int64_t n_tokens, const int32_t *cu_seqlens, int32_t n_
     return MROPE_OK;
 }
 
+struct Bytes {  // of an argument that a call reads or writes
+    const void *p;
+    int64_t n;
+};
+
+bool meet(const Bytes &a, const Bytes &b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.n > 0 && b.n > 0 && x < y + (uint64_t)b.n && y < x + (uint64_t)a.n;
+}
+
+// The same for n rows of `row` bytes, `stride` from one to the next.
+bool meet_rows(const Bytes &a, const void *p, int64_t n, int64_t row, int64_t stride)
+{
+    if (!p || a.n <= 0 || n <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(p);
+    const int64_t t = x > y ? std::min((int64_t)((x - y) / (uint64_t)stride), n - 1) : 0;  // the last that begins at or before a
+    for (int64_t i = t; i <= t + 1 && i < n; ++i)
+        if (meet(a, {reinterpret_cast<const void *>(y + (uint64_t)(i * stride)), row})) return true;
+    return false;
+}
+
+// Other workgroups still read what a workgroup's outputs would be written over.
+template <size_t NO, size_t NI>
+mrope_status check_outputs_apart(const Bytes (&out)[NO], const Bytes (&in)[NI])
+{
+    for (size_t i = 0; i < NO; ++i) {
+        for (size_t j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return fail(MROPE_ERR_ARG, "outputs must not overlap one another");
+        for (const Bytes &b : in)
+            if (meet(out[i], b)) return fail(MROPE_ERR_ARG, "outputs must not overlap inputs");
+    }
+    return MROPE_OK;
+}
+
 // The state of the page calls; fills `p`.
 mrope_status check_pages(int32_t *refcount, int64_t num_blocks, int32_t *tables, int64_t table_stride, int32_t table_width,
                          int32_t *lens, int64_t n_rows, int32_t block_size, int32_t n, Pages &p)
@@ -489,6 +524,10 @@ mrope_status mrope_planes_tree(const int32_t *parents, int64_t n_tokens, const i
     if ((int64_t)n_seqs * 256 > kMaxGridThreads) return fail(MROPE_ERR_ARG, "too many sequences (%d)", n_seqs);
     if (n_tokens == 0) return MROPE_OK;
     if (!parents || !pos_offset || !planes || !mask) return fail(MROPE_ERR_ARG, "parents / pos_offset / planes / mask is NULL");
+    const Bytes out[] = {{planes, n_tokens * 4}, {planes + plane_stride, n_tokens * 4}, {planes + 2 * plane_stride, n_tokens * 4},
+                         {mask, n_tokens * mask_words * 8}};
+    const Bytes in[] = {{parents, n_tokens * 4}, {cu_seqlens, (n_seqs + 1ll) * 4}, {pos_offset, n_seqs * 4ll}, {amount, amount ? n_seqs * 4ll : 0}};
+    if ((st = check_outputs_apart(out, in)) != MROPE_OK) return st;
     const PlanesTree a{parents, cu_seqlens, n_seqs, n_tokens, pos_offset, amount, planes, plane_stride, mask, mask_words};
     (void)hipGetLastError();
     return hip_status(launch_planes_tree(a, static_cast<hipStream_t>(stream)), "mrope_planes_tree");
@@ -523,6 +562,14 @@ mrope_status mrope_verify_tree(const void *target, int64_t target_stride, const 
     if (!n_kept || !next_ids || !u_next || !cu_seqlens) return fail(MROPE_ERR_ARG, "cu_seqlens / u_next / n_kept / next_ids is NULL");
     if (n_tokens > 0 && (!target || !ids || !u_accept || !path)) return fail(MROPE_ERR_ARG, "target / ids / u_accept / path is NULL");
     if ((st = check_workspace(workspace, workspace_bytes, verify_ws_bytes(n_seqs, plan))) != MROPE_OK) return st;
+    const Bytes out[] = {{n_kept, n_seqs * 4ll}, {path, n_tokens * 4}, {next_ids, n_seqs * 4ll}};
+    const Bytes in[] = {{ids, n_tokens * 4}, {parents, parents ? n_tokens * 4 : 0}, {cu_seqlens, (n_seqs + 1ll) * 4},
+                        {u_accept, n_tokens * 4}, {u_next, n_seqs * 4ll}};
+    if ((st = check_outputs_apart(out, in)) != MROPE_OK) return st;
+    for (const Bytes &o : out)
+        if (meet_rows(o, target, n_tokens, (int64_t)vocab * elem, target_stride * elem) ||
+            meet_rows(o, draft, n_tokens, (int64_t)vocab * elem, draft_stride * elem))
+            return fail(MROPE_ERR_ARG, "outputs must not overlap inputs");
     const Verify a{target, draft, target_stride, draft_stride, vocab, ids, parents, cu_seqlens, n_seqs, n_tokens,
                    u_accept, u_next, n_kept, path, next_ids};
     (void)hipGetLastError();

@@ -445,7 +445,7 @@ mrope_status mrope_attend_kv8(const void *q, int64_t q_tok_stride, int64_t q_hea
  *            and the parent's + 1 with one.
  * mask       [n_tokens][mask_words] uint64: bit b of word w of token i is set if token 64 w + b of its sequence is i
  *            or an ancestor of it (tokens past 64 * mask_words have no bit).  mask_words 1..16.
- * One launch.
+ * Neither output may overlap the other or an input.  One launch.
  * ------------------------------------------------------------------------------------------- */
 mrope_status mrope_planes_tree(const int32_t *parents, int64_t n_tokens, const int32_t *cu_seqlens, int32_t n_seqs,
                                const int32_t *pos_offset, const int32_t *amount, int32_t *planes, int64_t plane_stride,
@@ -496,7 +496,7 @@ mrope_status mrope_attend_tree_kv8(const void *q, int64_t q_tok_stride, int64_t 
  *
  * n_kept     [n_seqs] int32 out: accepted tokens, token 0 included (0 for an empty tree).
  * path       [n_tokens] int32 out: at cu_seqlens[s] + i the index of the i-th accepted token, -1 after the last.
- * next_ids   [n_seqs] int32 out (-1 for an empty tree).
+ * next_ids   [n_seqs] int32 out (-1 for an empty tree).  No output may overlap another or an input.
  * workspace  256-byte aligned, mrope_verify_tree_workspace_bytes(...) bytes, needing no initialisation; calls that share
  *            one must be ordered.
  * ------------------------------------------------------------------------------------------- */

@@ -6,7 +6,7 @@ import random
 
 import pytest
 
-from test_tree_abi_cpu import A, ARG, BASE, lib  # noqa: F401  (lib: a fixture)
+from test_tree_abi_cpu import A, ARG, BASE, _planes, _verify, lib  # noqa: F401  (lib: a fixture)
 
 
 # ---------------------------------------------------------------- keep --------------------------
@@ -94,3 +94,55 @@ def test_keep_layers_by_every_row(lib):  # noqa: F811
         assert apart(got) is fine, (nk, nb, strides, d)
         seen[fine] += 1
     assert min(seen) > 50
+
+
+# ---------------------------------------------------------------- planes and verification -------
+# 100 tokens of 4 sequences, each argument at a place of its own, 1 MB apart
+PLACES = {name: A << 4 | i << 20 for i, name in enumerate(["par", "cu", "pos", "am", "planes", "mask", "ids", "ua", "un", "nkept", "path", "nxt"])}
+FAR = dict(PLACES, t=1 << 40, d=1 << 41, dst=5000)
+VECTORS = dict(par=400, cu=20, pos=16, am=16, ids=400, ua=400, un=16, nkept=16, path=400, nxt=16)  # bytes
+
+
+def refused(st, message):
+    return st == ARG and "overlap" in message
+
+
+def planes(lib, **kw):  # noqa: F811
+    return refused(_planes(lib, **{**PLACES, **kw}), lib.mrope_last_error().decode())
+
+
+def verify(lib, **kw):  # noqa: F811
+    return refused(_verify(lib, **{**FAR, **kw}), lib.mrope_last_error().decode())
+
+
+@pytest.mark.parametrize("name", ["par", "cu", "pos", "am"])
+@pytest.mark.parametrize("out,size", [("planes", 400), ("mask", 1600)])
+def test_planes_over_its_inputs(lib, name, out, size):  # noqa: F811
+    at, n = PLACES[name], VECTORS[name]
+    assert planes(lib, **{out: at}) and planes(lib, **{out: at + (n - 4) // 8 * 8}) and planes(lib, **{out: at - size + 8})
+    if out == "planes":  # its second and third rows
+        assert planes(lib, planes=at - 4 * 5000, ps=5000) and planes(lib, planes=at - 8 * 5000 + n - 4, ps=5000)
+
+
+def test_planes_over_its_mask(lib):  # noqa: F811
+    assert planes(lib, mask=PLACES["planes"] + 1192) and planes(lib, mask=PLACES["planes"] - 1592)
+
+
+OUTPUTS = ["nkept", "path", "nxt"]
+
+
+@pytest.mark.parametrize("out,other", [(a, b) for a in OUTPUTS for b in ["par", "cu", "ids", "ua", "un", *OUTPUTS] if a != b])
+def test_verify_over_its_vectors(lib, out, other):  # noqa: F811
+    at = PLACES[other]
+    assert verify(lib, **{out: at}) and verify(lib, **{out: at + VECTORS[other] - 4}) and verify(lib, **{out: at - VECTORS[out] + 4})
+
+
+@pytest.mark.parametrize("out", OUTPUTS)
+@pytest.mark.parametrize("rows", ["t", "d"])
+def test_verify_over_its_rows(lib, out, rows):  # noqa: F811
+    base, n = FAR[rows], VECTORS[out]
+    kw = dict(tst=6000, dst=6000, v=5000)  # rows of 10,000 bytes, 2,000 between them
+    for row in (0, 1, 50, 99):
+        for at in (row * 12000, row * 12000 + 9996, row * 12000 - n + 4):
+            assert verify(lib, **{out: base + at}, **kw)
+
