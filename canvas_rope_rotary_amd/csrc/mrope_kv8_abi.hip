@@ -133,6 +133,37 @@ bool heads_overlap(const void *a, int64_t a_tok, int64_t a_head, const void *b, 
     return false;
 }
 
+struct Bytes {  // of an argument that a call reads or writes
+    const void *p;
+    int64_t n;
+};
+
+bool meet(const Bytes &a, const Bytes &b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.n > 0 && b.n > 0 && x < y + (uint64_t)b.n && y < x + (uint64_t)a.n;
+}
+
+// The same for n rows of `row` bytes, `stride` from one to the next.
+bool meet_rows(const Bytes &a, const void *p, int64_t n, int64_t row, int64_t stride)
+{
+    if (!p || a.n <= 0 || n <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(p);
+    if (stride == 0) n = 1;
+    const int64_t t = x > y && n > 1 ? std::min((int64_t)((x - y) / (uint64_t)stride), n - 1) : 0;  // the last that begins at or before a
+    for (int64_t i = t; i <= t + 1 && i < n; ++i)
+        if (meet(a, {reinterpret_cast<const void *>(y + (uint64_t)(i * stride)), row})) return true;
+    return false;
+}
+
+// The same for heads as above.
+bool meet_heads(const Bytes &a, const void *p, int64_t tok, int64_t head, int32_t n_heads, int64_t n_tokens, int64_t row_bytes, int64_t elem_bytes)
+{
+    for (int32_t h = 0; h < n_heads; ++h)
+        if (meet_rows(a, static_cast<const char *>(p) + h * head * elem_bytes, n_tokens, row_bytes, tok * elem_bytes)) return true;
+    return false;
+}
+
 Kv8 make_kv8(const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale, int64_t num_blocks,
              int64_t c_block, int64_t c_tok, int64_t c_head, int32_t nk, const int32_t *tables, int64_t table_stride,
              int32_t table_width, int32_t block_size)
@@ -283,28 +314,6 @@ mrope_status check_trees(int64_t n_tokens, const int32_t *cu_seqlens, int32_t n_
     if (!aligned(cu_seqlens, 4)) return fail(MROPE_ERR_ALIGN, "cu_seqlens must be 4-byte aligned");
     if (n_tokens > 0 && !cu_seqlens) return fail(MROPE_ERR_ARG, "cu_seqlens is NULL");
     return MROPE_OK;
-}
-
-struct Bytes {  // of an argument that a call reads or writes
-    const void *p;
-    int64_t n;
-};
-
-bool meet(const Bytes &a, const Bytes &b)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.n > 0 && b.n > 0 && x < y + (uint64_t)b.n && y < x + (uint64_t)a.n;
-}
-
-// The same for n rows of `row` bytes, `stride` from one to the next.
-bool meet_rows(const Bytes &a, const void *p, int64_t n, int64_t row, int64_t stride)
-{
-    if (!p || a.n <= 0 || n <= 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(p);
-    const int64_t t = x > y ? std::min((int64_t)((x - y) / (uint64_t)stride), n - 1) : 0;  // the last that begins at or before a
-    for (int64_t i = t; i <= t + 1 && i < n; ++i)
-        if (meet(a, {reinterpret_cast<const void *>(y + (uint64_t)(i * stride)), row})) return true;
-    return false;
 }
 
 // Other workgroups still read what a workgroup's outputs would be written over.
@@ -504,6 +513,15 @@ mrope_status mrope_attend_tree_kv8(const void *q, int64_t q_tok_stride, int64_t 
     if (!aligned(mask, 8) || !aligned(context_lens, 4)) return fail(MROPE_ERR_ALIGN, "mask must be 8-byte, context_lens 4-byte aligned");
     if (a.n_tokens == 0) return MROPE_OK;
     if (!mask) return fail(MROPE_ERR_ARG, "mask is NULL");
+    const int64_t elem = dtype == MROPE_F32 ? 4 : 2, row = head_dim * elem;
+    const Bytes z = {lse, lse ? n_tokens * n_q_heads * 4 : 0};
+    const Bytes in[] = {{cu_seqlens, (n_seqs + 1ll) * 4}, {context_lens, n_seqs * 4ll}, {mask, n_tokens * mask_words * 8}};
+    if (meet_heads(z, q, q_tok_stride, q_head_stride, n_q_heads, n_tokens, row, elem) ||
+        meet_heads(z, out, out_tok_stride, out_head_stride, n_q_heads, n_tokens, row, elem))
+        return fail(MROPE_ERR_ARG, "lse must not overlap q or out");
+    for (const Bytes &b : in)
+        if (meet(z, b) || meet_heads(b, out, out_tok_stride, out_head_stride, n_q_heads, n_tokens, row, elem))
+            return fail(MROPE_ERR_ARG, "out and lse must not overlap cu_seqlens, context_lens or mask");
     a.mask = mask;
     a.mask_words = mask_words;
     (void)hipGetLastError();

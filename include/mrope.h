@@ -459,6 +459,7 @@ mrope_status mrope_planes_tree(const int32_t *parents, int64_t n_tokens, const i
  * the sequence whose bit is set in
  * mask       [n_tokens][mask_words] uint64 (mrope_planes_tree's, or any other: a token need not see itself, or
  *            may see later ones).  Tokens without a bit are not seen.  mask_words 1..64.
+ * out and lse overlap neither one another nor q, cu_seqlens, context_lens or mask.
  * cache_tok_stride is below 2^28, and (n_tokens * n_q_heads / n_kv_heads / 32 + n_seqs + 1024) * n_kv_heads at most
  * 2^23 (tiles of 32 rows of all sequences and KV heads).
  * ------------------------------------------------------------------------------------------- */

@@ -68,3 +68,26 @@ def test_planes_refuse_their_inputs_place():
     mask = torch.as_strided(flat, (12,), (1,), 28).view(torch.int64).view(6, 1)  # between the first two rows
     got = mr.planes_tree(parents, cu, pos, planes=planes, mask=mask)
     assert [x.tolist() for x in got] == want
+
+
+def test_attend_refuses_its_inputs_place():
+    """Outputs in the place of the mask, the lengths or one another: refused.  Log-sums in the gap between two rows of queries: the
+    same as anywhere."""
+    w = World([40], 16, 2, 128, seed=83)
+    room = torch.zeros(7, 9, 128, device="cuda")
+    q = room[:, :8]
+    q.copy_(w.heads(7, 8, "f32"))
+    cu, ctx, tab, cache = i32([0, 7]).cuda(), i32([40]).cuda(), w.tables.cuda(), w.cache()
+    mask = torch.full((7, 28), -1, dtype=torch.int64, device="cuda")
+    out, lse = mr.attend_tree_kv8(q, cu, ctx, mask, tab, *cache, return_lse=True)
+    for bad in (mask.view(torch.float32).view(-1)[:56].view(7, 8), room[3, 7][:56].view(7, 8)):
+        with pytest.raises(mr.MropeError, match="overlap"):
+            mr.attend_tree_kv8(q, cu, ctx, mask, tab, *cache, lse=bad)
+    big = torch.zeros(7 * 8 * 128 + 64, device="cuda")
+    with pytest.raises(mr.MropeError, match="overlap"):
+        mr.attend_tree_kv8(q, cu, ctx, mask, tab, *cache, out=big[:7168].view(7, 8, 128), lse=big[7120:7176].view(7, 8))
+    with pytest.raises(mr.MropeError, match="overlap"):
+        mr.attend_tree_kv8(q, cu, ctx, big[6000:6014].view(torch.int64).view(7, 1), tab, *cache, out=big[:7168].view(7, 8, 128))
+    gap = room[2, 8][:56].view(7, 8)
+    o2, z2 = mr.attend_tree_kv8(q, cu, ctx, mask, tab, *cache, lse=gap)
+    assert z2 is gap and torch.equal(o2, out) and torch.equal(z2, lse)

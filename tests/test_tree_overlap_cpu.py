@@ -6,7 +6,7 @@ import random
 
 import pytest
 
-from test_tree_abi_cpu import A, ARG, BASE, _planes, _verify, lib  # noqa: F401  (lib: a fixture)
+from test_tree_abi_cpu import A, ARG, BASE, _attend, _planes, _verify, lib  # noqa: F401  (lib: a fixture)
 
 
 # ---------------------------------------------------------------- keep --------------------------
@@ -146,3 +146,30 @@ def test_verify_over_its_rows(lib, out, rows):  # noqa: F811
         for at in (row * 12000, row * 12000 + 9996, row * 12000 - n + 4):
             assert verify(lib, **{out: base + at}, **kw)
 
+
+
+# ---------------------------------------------------------------- attention ---------------------
+# (rows of out and q: 8 heads of 512 bytes a token, 256 bytes between them)
+SPARSE = dict(q=1 << 40, out=1 << 41, qt=8 * 384, qh=384, ot=8 * 384, oh=384)
+
+
+def attend(lib, **kw):  # noqa: F811
+    st = _attend(lib, **{**{k: PLACES[k] for k in ("cu", "mask")}, "ctx": PLACES["pos"], **SPARSE, **kw})
+    return st == ARG and "overlap" in lib.mrope_last_error().decode()
+
+
+@pytest.mark.parametrize("name,size", [("cu", 20), ("ctx", 16), ("mask", 1600)])
+def test_attend_over_its_vectors(lib, name, size):  # noqa: F811
+    at = 1 << 42
+    for d in (0, size - 4, 4 - 3200):
+        assert attend(lib, **{name: at, "lse": at + d})
+    for row in (0, 7, 8 * 99 + 3):
+        for d in (0, 504, -((size - 4) // 8 * 8)):
+            assert attend(lib, **{name: SPARSE["out"] + 768 * row + d})
+
+
+@pytest.mark.parametrize("name", ["q", "out"])
+def test_attend_lse_over_rows(lib, name):  # noqa: F811
+    for row in (0, 7, 8 * 99 + 7):
+        for d in (0, 508, 4 - 3200):
+            assert attend(lib, lse=SPARSE[name] + 768 * row + d)
