@@ -48,6 +48,7 @@ mrope_status check_kv8(const void *k_cache, const void *v_cache, const float *k_
 
 struct Dim {
     int64_t stride, extent;
+    int64_t span;  // of the rows of one index: by the strides below it
     bool operator<(const Dim &o) const { return stride < o.stride; }
 };
 
@@ -56,7 +57,7 @@ struct Dim {
 mrope_status check_rows_apart(int64_t num_blocks, int64_t c_block, int32_t block_size, int64_t c_tok, int32_t nk, int64_t c_head,
                               int32_t head_dim)
 {
-    Dim dims[3] = {{c_block, num_blocks}, {c_tok, block_size}, {c_head, nk}};
+    Dim dims[3] = {{c_block, num_blocks, 0}, {c_tok, block_size, 0}, {c_head, nk, 0}};
     std::sort(dims, dims + 3);
     int64_t span = head_dim;
     for (const auto &d : dims) {
@@ -73,10 +74,10 @@ bool rows_meet(const Dim *dims, int n, int64_t d, int32_t head_dim)
 {
     if (n == 0) return d < head_dim && -d < head_dim;
     const Dim &top = dims[n - 1];
-    const int64_t k = d >= 0 ? d / top.stride : -((-d + top.stride - 1) / top.stride);
-    for (int64_t i = k; i <= k + 1; ++i)
-        if (i < top.extent && -i < top.extent && rows_meet(dims, n - 1, d - i * top.stride, head_dim)) return true;
-    return false;
+    int64_t k = d >= 0 && d < top.stride ? 0 : d / top.stride, r = d - k * top.stride;
+    if (r < 0) --k, r += top.stride;
+    return (r < top.span && k < top.extent && -k < top.extent && rows_meet(dims, n - 1, r, head_dim)) ||
+           (top.stride - r < top.span && k + 1 < top.extent && -k - 1 < top.extent && rows_meet(dims, n - 1, r - top.stride, head_dim));
 }
 
 // Calls that write the caches of several layers at once do so from waves of their own for each cache and head: no
@@ -85,13 +86,17 @@ mrope_status check_layers_apart(const mrope_kv8_layer *layers, int32_t n_layers,
                                 int32_t block_size, int64_t c_tok, int32_t nk, int64_t c_head, int32_t head_dim)
 {
     if (num_blocks == 0) return MROPE_OK;
-    const Dim all[3] = {{c_block, num_blocks}, {c_tok, block_size}, {c_head, nk}};
+    const Dim all[3] = {{c_block, num_blocks, 0}, {c_tok, block_size, 0}, {c_head, nk, 0}};
     Dim dims[3];
     int n_dims = 0;
-    uint64_t span = head_dim;
     for (const auto &d : all)
-        if (d.extent > 1) dims[n_dims++] = d, span += (uint64_t)((d.extent - 1) * d.stride);
+        if (d.extent > 1) dims[n_dims++] = d;
     std::sort(dims, dims + n_dims);
+    int64_t span = head_dim;
+    for (int i = 0; i < n_dims; ++i) {
+        dims[i].span = span;
+        span += (dims[i].extent - 1) * dims[i].stride;
+    }
     uintptr_t codes[2 * MROPE_MAX_LAYERS], scales[2 * MROPE_MAX_LAYERS];
     const int n = 2 * n_layers;
     for (int i = 0; i < n; ++i) {
@@ -102,7 +107,7 @@ mrope_status check_layers_apart(const mrope_kv8_layer *layers, int32_t n_layers,
     std::sort(codes, codes + n);
     std::sort(scales, scales + n);
     for (int i = 0; i < n; ++i)
-        for (int j = i + 1; j < n && codes[j] - codes[i] < span; ++j)
+        for (int j = i + 1; j < n && codes[j] - codes[i] < (uint64_t)span; ++j)
             if (rows_meet(dims, n_dims, (int64_t)(codes[j] - codes[i]), head_dim))
                 return fail(MROPE_ERR_ARG, "caches of different layers, or K's and V's of one, share rows");
     for (int i = 0; i + 1 < n; ++i)
