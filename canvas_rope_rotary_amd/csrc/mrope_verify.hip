@@ -272,13 +272,6 @@ __device__ __forceinline__ double wave_scan(double x)
     return x;
 }
 
-__device__ __forceinline__ double last_lane(double x)
-{
-    const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
 // Sums over the workgroup of the threads up to this one's, and of all of them.
 __device__ double block_scan(double x, double &all, Shared &sh)
 {
