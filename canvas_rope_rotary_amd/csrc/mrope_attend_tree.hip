@@ -21,10 +21,14 @@
 //
 // Only blocks that reach past ctx - len, or into a page that is not there, look at the mask.
 //
-// Measured, heads of 256 in bf16, 8 of 2 KV heads: 64 trees of 32 tokens at 4,096 positions 122 us and the join, 103 GFLOP
-// with P's second term, 0.84 PFLOP/s; the matrix instructions are busy for 47 % of the time and the others, decoding and
-// the softmax, for as much: on the two waves of a SIMD the sum of both is 95 % of the cycles.  8 trees of 16 at 32,000
-// positions: 72 us and the join's 6, 263 MB of codes (3.7 TB/s).  A call of one tree at a short context is a chain of
+// Measured, heads of 256 in bf16, 8 of 2 KV heads (a call, and the medians of its kernels under a trace): 64 trees of 32 tokens
+// at 4,096 positions 119 us (128 + 4.9 for a join with nothing to join), 103 GFLOP with P's second term, 0.87 PFLOP/s; 8 trees
+// of 16 at 32,000 positions 73 us (79 + 6.8), 263 MB of codes, 3.6 TB/s.  The matrix instructions are busy for
+// 45 % of a wave's cycles (99,000 of 221,000; of the latter's 33 %) and the others, decoding and the softmax, issue for about as
+// many, few of them at the same time: scores, softmax and product of a block follow one another, in both waves of a SIMD.  That
+// is the order they are written in and no limit of the hardware: in a loop of one 32 x 32 x 16 instruction and three conversions
+// two waves take 19.0 ns a step, where the two kinds alone take 14.7 and 14.1.  fp32, three terms of both (207 GFLOP for the 64 trees):
+// 214 us, 0.97 PFLOP/s, heads of 128 110, of 64 65.  A call of one tree at a short context is a chain of
 // waits, 12 us: 2 to find the chunk, 3 for the page's number, then its codes and scales, 1 for the queries, 2 for a block,
 // 4 for the parts to meet, most of them for code that comes for the first time.
 #include <algorithm>

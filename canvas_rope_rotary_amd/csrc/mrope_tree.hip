@@ -12,7 +12,9 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // ------------------------------------------------------------------ planes and masks -----------
 // A workgroup a sequence, a thread a token, the sequence's parents in LDS.  A token's ancestors come in descending
 // order (a parent comes before its children), so the words of its mask are finished one after the other.
-// Bound: latency, a read of LDS for each step to the root.  A tree of 8 tokens takes 2.0 us, 512 of 64 4.2 us.
+// Bound: latency, a read of LDS for each step to the root.  A tree of 8 tokens takes 2.0 us, 512 random ones of 64 4.2 and 32 of
+// 1,024 17.  Deep trees take a time that grows with their depth: 512 chains of 64 10.8 us, one chain of 1,024, or 32 of
+// them, 365 to 371 (a thread takes four of the tokens, 2,560 steps of some 290 cycles for the last).
 constexpr int kPlanesThreads = 256;
 
 __global__ __launch_bounds__(kPlanesThreads) void planes_tree_kernel(PlanesTree a)
