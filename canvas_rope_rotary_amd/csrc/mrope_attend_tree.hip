@@ -22,8 +22,8 @@
 // Only blocks that reach past ctx - len, or into a page that is not there, look at the mask.
 //
 // Measured, heads of 256 in bf16, 8 of 2 KV heads (a call, and the medians of its kernels under a trace): 64 trees of 32 tokens
-// at 4,096 positions 119 us (128 + 4.9 for a join with nothing to join), 103 GFLOP with P's second term, 0.87 PFLOP/s; 8 trees
-// of 16 at 32,000 positions 73 us (79 + 6.8), 263 MB of codes, 3.6 TB/s.  The matrix instructions are busy for
+// at 4,096 positions 119 to 121 us (128 + 4.9 for a join with nothing to join), 103 GFLOP with P's second term, 0.87 PFLOP/s; 8 trees
+// of 16 at 32,000 positions 73 to 79 us (79 + 6.8), 263 MB of codes, 3.3 to 3.6 TB/s.  The matrix instructions are busy for
 // 45 % of a wave's cycles (99,000 of 221,000; of the latter's 33 %) and the others, decoding and the softmax, issue for about as
 // many, few of them at the same time: scores, softmax and product of a block follow one another, in both waves of a SIMD.  That
 // is the order they are written in and no limit of the hardware: in a loop of one 32 x 32 x 16 instruction and three conversions
